@@ -73,7 +73,8 @@ LOKI_API const char* loki_last_error(void);
 /*
  * Kernel error word of the current device: 1 if a staged kernel's bounded
  * wait on an asynchronous copy gave up, 2 if a paged call met a block-table
- * entry outside the page pool (the results of the call are then invalid). Synchronous: copies 4 bytes from the device (waiting for prior
+ * entry outside the page pool (the results of the call are then invalid), 3 if
+ * an append met a position behind its rope table. Synchronous: copies 4 bytes from the device (waiting for prior
  * work); with reset != 0 the word is cleared afterwards.
  */
 LOKI_API loki_status loki_device_error(int* code, int reset);
@@ -300,6 +301,134 @@ LOKI_API loki_status loki_append_keys_paged(const void* K_new, const void* V_new
                                             const int32_t* positions, int B, int H_kv, int T,
                                             int page_size, int max_pages, int64_t n_pages, int D,
                                             loki_dtype dt, void* stream);
+
+/* Paged appends with the rotary embedding, and 8-bit pages ------------------- */
+/*
+ * Token positions as the paged calls above define them: token t of sequence b
+ * gets index j = positions[b] + t, which is also its rotary position. The
+ * Loki pages rotate keys after the rotary embedding (poster page, "More on
+ * figures": post-rotary PCA); these appends take the model's keys before it
+ * and apply both on the way into the cache.
+ *
+ * 8-bit pages (an 8-bit cache is not in the Loki pages: a storage choice of
+ * this library): e4m3 codes [n_pages, H_kv, page_size, D] and one fp32 scale
+ * for each block of `block` consecutive tokens of a (page, KV head),
+ * [n_pages, H_kv, page_size / block]; the cached value is code * scale. block
+ * is 16, 32, 64 or 128 and divides page_size. The append writes powers of two:
+ * the least 2^e (e >= -126) with amax <= 448 * 2^e over the block's tokens.
+ */
+
+/*
+ * table [n_pos, rot_dim] fp32 of the rotary embedding's angles: row j holds
+ * cos(a_i) in columns i < rot_dim / 2 and sin(a_i) in columns rot_dim / 2 + i,
+ * a_i = j * pos_scale * base^(-2 i / rot_dim), computed in fp64 and rounded
+ * once. rot_dim is a multiple of 16, at most 128; base > 0.
+ */
+LOKI_API loki_status loki_rope_table(float* table, int64_t n_pos, int rot_dim, double base,
+                                     double pos_scale, void* stream);
+
+/*
+ * loki_append_keys_paged with the rotary embedding on the way: the new keys
+ * are turned by their positions' angles and then rotated into the basis,
+ * K~ = rope(K_new) P (all fp32, one rounding to dt); values are copied.
+ *   K_new, V_new [B, H_kv, T, D] (dt)
+ *   P            [H_kv, D, D] fp32, or NULL: no basis, K~ = rope(K_new)
+ *   rope_table   [n_pos, rot_dim] fp32 as loki_rope_table writes it (or any
+ *                other angles), or NULL: no rotary embedding. Columns i and
+ *                i + rot_dim / 2 form a pair (interleaved == 0), or columns
+ *                2 i and 2 i + 1 (interleaved != 0); columns >= rot_dim stay.
+ *                rot_dim a multiple of 16, at most D.
+ *   q, q_out     [B, H_q, T, D] (dt), both or neither: the step's queries,
+ *                turned by the same angles and rounded once (not rotated into
+ *                the basis: the decode does that). q_out may be q.
+ *   Kt_lo_pages  [n_pages, H_kv, page_size, d_lo] (dt) or NULL
+ *   new_lens     [B] int32 device array or NULL: only the first new_lens[b]
+ *                (clamped to [0, T]) tokens of sequence b are appended; the
+ *                others' rows, q_out's among them, are left as they were.
+ * Tokens outside the block table, in a page outside the pool (device error 2)
+ * or at positions >= n_pos (device error 3) are not written. No two appended
+ * tokens may share a cache row. No workspace.
+ */
+LOKI_API loki_status loki_append_keys_paged_rope(
+    const void* K_new, const void* V_new, const float* P, const float* rope_table, int64_t n_pos,
+    int rot_dim, int interleaved, const void* q, void* q_out, int H_q, void* Kt_pages,
+    void* V_pages, void* Kt_lo_pages, int d_lo, const int32_t* block_table,
+    const int32_t* positions, const int32_t* new_lens, int B, int H_kv, int T, int page_size,
+    int max_pages, int64_t n_pages, int D, loki_dtype dt, void* stream);
+
+/*
+ * The same append into 8-bit pages: K~ and V_new are stored as code =
+ * e4m3(x / scale), nearest even (infinities saturate at 448, NaN stays NaN and
+ * neither counts in amax). A block that already holds tokens of the sequence
+ * (its rows before positions[b]) keeps its scale unless the new tokens need a
+ * larger one; its older codes are then moved to the new scale, which is exact
+ * except where a code falls among e4m3's subnormals. A block whose first row
+ * is appended starts afresh, whatever its page held before: pages need no
+ * clearing between sequences. The plane is written in dt, from the unrounded
+ * keys. A block may receive tokens of one sequence only. dt is the type of
+ * K_new, V_new, q and the plane. Other arguments as
+ * loki_append_keys_paged_rope.
+ */
+LOKI_API loki_status loki_append_keys_paged_q8(
+    const void* K_new, const void* V_new, const float* P, const float* rope_table, int64_t n_pos,
+    int rot_dim, int interleaved, const void* q, void* q_out, int H_q, void* K8_pages,
+    void* V8_pages, float* k_scales, float* v_scales, int block, void* Kt_lo_pages, int d_lo,
+    const int32_t* block_table, const int32_t* positions, const int32_t* new_lens, int B, int H_kv,
+    int T, int page_size, int max_pages, int64_t n_pages, int D, loki_dtype dt, void* stream);
+
+/* Bytes of workspace dense_decode_attention_paged_q8 needs (split partials). */
+LOKI_API size_t dense_decode_paged_q8_workspace_size(int B, int H_q, int H_kv, int page_size,
+                                                     int max_pages, int D);
+
+/*
+ * Full attention of one query token per sequence over its seq_lens[b] cached
+ * tokens (device array, int32, clamped to [0, page_size * max_pages]) in 8-bit
+ * pages: the cached keys and values are code * scale (scales finite, >= 0).
+ *   q, out [B, H_q, D] (dt); scale <= 0 selects 1/sqrt(D)
+ * q and the cached keys are both in the PCA basis or both not. Tokens in pages
+ * outside the pool are skipped (device error 2); a sequence without tokens
+ * gives zeros. Scores, softmax and sums in fp32.
+ */
+LOKI_API loki_status dense_decode_attention_paged_q8(
+    const void* q, const void* K8_pages, const void* V8_pages, const float* k_scales,
+    const float* v_scales, int block, const int32_t* block_table, const int32_t* seq_lens, int B,
+    int H_q, int H_kv, int page_size, int max_pages, int64_t n_pages, int D, float scale,
+    loki_dtype dt, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace loki_sparse_attention_paged_q8 needs (split partials). */
+LOKI_API size_t loki_sparse_attention_paged_q8_workspace_size(int B, int H_q, int H_kv, int64_t k,
+                                                              int D);
+
+/*
+ * loki_sparse_attention over 8-bit pages: exact attention of each (sequence,
+ * query head) over the tokens its row of selected_idx [B, H_q, k] names.
+ * Entries outside [0, seq_lens[b]) are skipped, an entry counts as often as it
+ * occurs, a row without valid entries gives zeros.
+ *   q_rot [B, H_q, D] fp32;  out [B, H_q, D] (dt)
+ */
+LOKI_API loki_status loki_sparse_attention_paged_q8(
+    const float* q_rot, const void* K8_pages, const void* V8_pages, const float* k_scales,
+    const float* v_scales, int block, const int32_t* block_table, const int32_t* seq_lens,
+    const int32_t* selected_idx, int B, int H_q, int H_kv, int page_size, int max_pages,
+    int64_t n_pages, int D, int64_t k, float scale, loki_dtype dt, void* out, void* ws,
+    size_t ws_bytes, void* stream);
+
+/* Bytes of workspace loki_decode_attention_paged_q8 needs. */
+LOKI_API size_t loki_paged_q8_decode_workspace_size(int B, int H_q, int H_kv, int page_size,
+                                                    int max_pages, int D, int d, int64_t k);
+
+/*
+ * loki_decode_attention_paged over 8-bit pages: the selection is the same (it
+ * reads the plane, which is in dt), the attention over the selected tokens
+ * reads all D columns of the 8-bit keys. Arguments, limits and results
+ * otherwise as loki_decode_attention_paged.
+ */
+LOKI_API loki_status loki_decode_attention_paged_q8(
+    const void* q, const void* K8_pages, const void* V8_pages, const float* k_scales,
+    const float* v_scales, int block, const void* Kt_lo_pages, int d_lo, const float* P,
+    const int32_t* block_table, const int32_t* seq_lens, int B, int H_q, int H_kv, int page_size,
+    int max_pages, int64_t n_pages, int D, int d, int64_t k, float scale, loki_dtype dt, void* out,
+    int32_t* selected_idx, void* ws, size_t ws_bytes, void* stream);
 
 /* Steps of loki_decode_attention, callable one by one ------------------- */
 

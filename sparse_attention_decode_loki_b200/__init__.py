@@ -13,6 +13,7 @@ top k are kept, and exact softmax attention runs over those k tokens only.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -31,6 +32,10 @@ __all__ = [
     "loki_decode_workspace_size", "dense_decode_workspace_size",
     "loki_sparse_attention_workspace_size", "loki_calibrate_workspace_size",
     "loki_topk_workspace_size", "loki_device_error",
+    "loki_rope_table", "loki_append_keys_paged_rope", "loki_append_keys_paged_q8",
+    "dense_decode_attention_paged_q8", "dense_decode_paged_q8_workspace_size",
+    "loki_sparse_attention_paged_q8", "loki_sparse_attention_paged_q8_workspace_size",
+    "loki_decode_attention_paged_q8", "loki_paged_q8_decode_workspace_size",
 ]
 
 
@@ -352,6 +357,284 @@ def loki_append_keys_paged(K_new: torch.Tensor, V_new: torch.Tensor, P: torch.Te
                                      block_table.data_ptr(), positions.data_ptr(), B, H_kv, T,
                                      page_size, block_table.shape[1], n_pages, D, _dt(K_new),
                                      _stream(dev)), "loki_append_keys_paged")
+
+
+# ---------------------------------------------------------------------------
+# paged appends with the rotary embedding, 8-bit pages
+# ---------------------------------------------------------------------------
+
+def _on(dev: torch.device):
+    """Makes the tensors' device the current one for the library's launches."""
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def loki_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, pos_scale: float = 1.0,
+                    device: Optional[torch.device] = None,
+                    table: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rotary angles' cos and sin, [n_pos, rot_dim] fp32: row j holds cos(j * pos_scale *
+    base^(-2i/rot_dim)) in column i and the sin in column rot_dim/2 + i."""
+    if table is None:
+        table = torch.empty((n_pos, rot_dim), dtype=torch.float32,
+                            device="cuda" if device is None else device)
+    dev = _cuda(table)
+    _expect(table, (n_pos, rot_dim), torch.float32, "table")
+    with _on(dev):
+        check(lib.loki_rope_table(table.data_ptr(), n_pos, rot_dim, base, pos_scale, _stream(dev)),
+              "loki_rope_table")
+    return table
+
+
+def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rope_table, plane,
+                  new_lens, q, q_out):
+    """What the two rotary appends share: (device, shapes, q_out, the C arguments around the pages)."""
+    ts = [K_new, V_new, K_pages, V_pages, block_table, positions]
+    for t in (P, rope_table, plane, new_lens, q, q_out):
+        if t is not None:
+            ts.append(t)
+    dev = _cuda(*ts)
+    if K_new.dim() != 4 or K_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("K_new [B, H_kv, T, D], pages [n_pages, H_kv, page_size, D] and "
+                         "block_table [B, max_pages] expected")
+    B, H_kv, T, D = K_new.shape
+    n_pages, Hp, page_size, Dp = K_pages.shape
+    if (V_new.shape != K_new.shape or V_pages.shape != K_pages.shape or Hp != H_kv or Dp != D
+            or block_table.shape[0] != B or tuple(positions.shape) != (B,)):
+        raise ValueError("K_new, V_new [B, H_kv, T, D], the pages, block_table [B, max_pages] and "
+                         "positions [B] disagree")
+    if block_table.dtype != torch.int32 or positions.dtype != torch.int32:
+        raise TypeError("block_table and positions must be int32")
+    dt = _dt(K_new)
+    if V_new.dtype != K_new.dtype or V_pages.dtype != K_pages.dtype:
+        raise TypeError("K_new and V_new, and the two page pools, must share a dtype")
+    if P is not None:
+        _expect(P, (H_kv, D, D), torch.float32, "P")
+    if rope_table is not None and (rope_table.dim() != 2 or rope_table.dtype != torch.float32):
+        raise ValueError("rope_table must be float32 [n_pos, rot_dim]")
+    if plane is not None:
+        if plane.dim() != 4:
+            raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
+        _expect(plane, (n_pages, H_kv, page_size, plane.shape[3]), K_new.dtype, "Kt_lo_pages")
+    if new_lens is not None:
+        _expect(new_lens, (B,), torch.int32, "new_lens")
+    H_q = H_kv
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must be [B, H_q, T, D]")
+        H_q = q.shape[1]
+        _expect(q, (B, H_q, T, D), K_new.dtype, "q")
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _expect(q_out, q.shape, q.dtype, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    front = (K_new.data_ptr(), V_new.data_ptr(), None if P is None else P.data_ptr(),
+             *((None, 0, 0) if rope_table is None else
+               (rope_table.data_ptr(), rope_table.shape[0], rope_table.shape[1])))
+    back = (None if plane is None else plane.data_ptr(), 0 if plane is None else plane.shape[3],
+            block_table.data_ptr(), positions.data_ptr(),
+            None if new_lens is None else new_lens.data_ptr(), B, H_kv, T, page_size,
+            block_table.shape[1], n_pages, D, dt)
+    return dev, H_q, q_out, front, back
+
+
+def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
+                                Kt_pages: torch.Tensor, V_pages: torch.Tensor,
+                                block_table: torch.Tensor, positions: torch.Tensor,
+                                rope_table: Optional[torch.Tensor] = None,
+                                interleaved: bool = False,
+                                Kt_lo_pages: Optional[torch.Tensor] = None,
+                                new_lens: Optional[torch.Tensor] = None,
+                                q: Optional[torch.Tensor] = None,
+                                q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Append rope(K_new) P and V_new [B, H_kv, T, D] at tokens positions[b] + t of the page pool,
+    and turn the queries q [B, H_q, T, D] by the same angles; returns q_out (None without q).
+    P None: no basis; rope_table None: no rotary embedding; new_lens [B] int32: only the first
+    new_lens[b] tokens (see include/loki.h)."""
+    dev, H_q, q_out, front, back = _check_append(K_new, V_new, P, Kt_pages, V_pages, block_table,
+                                                 positions, rope_table, Kt_lo_pages, new_lens, q,
+                                                 q_out)
+    if Kt_pages.dtype != K_new.dtype:
+        raise TypeError("K_new and the pages must share a dtype")
+    with _on(dev):
+        check(lib.loki_append_keys_paged_rope(*front, int(interleaved),
+                                              None if q is None else q.data_ptr(),
+                                              None if q is None else q_out.data_ptr(), H_q,
+                                              Kt_pages.data_ptr(), V_pages.data_ptr(), *back,
+                                              _stream(dev)), "loki_append_keys_paged_rope")
+    return q_out
+
+
+def _check_q8(K8_pages, V8_pages, k_scales, v_scales):
+    """(block) of 8-bit pages and their scales."""
+    if K8_pages.dtype != torch.float8_e4m3fn or V8_pages.dtype != torch.float8_e4m3fn:
+        raise TypeError("8-bit pages must be torch.float8_e4m3fn")
+    if K8_pages.dim() != 4 or V8_pages.shape != K8_pages.shape or k_scales.dim() != 3:
+        raise ValueError("pages [n_pages, H_kv, page_size, D] and scales [n_pages, H_kv, "
+                         "page_size / block] expected")
+    n_pages, H_kv, page_size, _ = K8_pages.shape
+    nb = k_scales.shape[2]
+    if nb < 1 or page_size % nb:
+        raise ValueError("page_size must be a multiple of the scales' blocks per page")
+    _expect(k_scales, (n_pages, H_kv, nb), torch.float32, "k_scales")
+    _expect(v_scales, (n_pages, H_kv, nb), torch.float32, "v_scales")
+    return page_size // nb
+
+
+def loki_append_keys_paged_q8(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
+                              K8_pages: torch.Tensor, V8_pages: torch.Tensor,
+                              k_scales: torch.Tensor, v_scales: torch.Tensor,
+                              block_table: torch.Tensor, positions: torch.Tensor,
+                              rope_table: Optional[torch.Tensor] = None, interleaved: bool = False,
+                              Kt_lo_pages: Optional[torch.Tensor] = None,
+                              new_lens: Optional[torch.Tensor] = None,
+                              q: Optional[torch.Tensor] = None,
+                              q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """loki_append_keys_paged_rope into 8-bit pages: e4m3 codes [n_pages, H_kv, page_size, D]
+    (torch.float8_e4m3fn) with fp32 scales [n_pages, H_kv, page_size / block], powers of two."""
+    block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
+    dev, H_q, q_out, front, back = _check_append(K_new, V_new, P, K8_pages, V8_pages, block_table,
+                                                 positions, rope_table, Kt_lo_pages, new_lens, q,
+                                                 q_out)
+    _cuda(K_new, k_scales, v_scales)
+    with _on(dev):
+        check(lib.loki_append_keys_paged_q8(*front, int(interleaved),
+                                            None if q is None else q.data_ptr(),
+                                            None if q is None else q_out.data_ptr(), H_q,
+                                            K8_pages.data_ptr(), V8_pages.data_ptr(),
+                                            k_scales.data_ptr(), v_scales.data_ptr(), block, *back,
+                                            _stream(dev)), "loki_append_keys_paged_q8")
+    return q_out
+
+
+def dense_decode_paged_q8_workspace_size(B: int, H_q: int, H_kv: int, page_size: int,
+                                         max_pages: int, D: int) -> int:
+    return int(lib.dense_decode_paged_q8_workspace_size(B, H_q, H_kv, page_size, max_pages, D))
+
+
+def loki_sparse_attention_paged_q8_workspace_size(B: int, H_q: int, H_kv: int, k: int,
+                                                  D: int) -> int:
+    return int(lib.loki_sparse_attention_paged_q8_workspace_size(B, H_q, H_kv, k, D))
+
+
+def loki_paged_q8_decode_workspace_size(B: int, H_q: int, H_kv: int, page_size: int,
+                                        max_pages: int, D: int, d: int, k: int) -> int:
+    return int(lib.loki_paged_q8_decode_workspace_size(B, H_q, H_kv, page_size, max_pages, D, d, k))
+
+
+def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace):
+    """What the attentions over 8-bit pages share: (device, sizes of the C call)."""
+    block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
+    dev = _cuda(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens,
+                *(() if workspace is None else (workspace,)))
+    n_pages, H_kv, page_size, D = K8_pages.shape
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q [B, H_q, D] and block_table [B, max_pages] expected")
+    B, H_q, Dq = q.shape
+    if Dq != D or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("q [B, H_q, D], block_table [B, max_pages], seq_lens [B] disagree")
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_table and seq_lens must be int32")
+    return dev, B, H_q, H_kv, page_size, block_table.shape[1], n_pages, D, block
+
+
+def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
+                                    V8_pages: torch.Tensor, k_scales: torch.Tensor,
+                                    v_scales: torch.Tensor, block_table: torch.Tensor,
+                                    seq_lens: torch.Tensor, scale: float = 0.0,
+                                    out: Optional[torch.Tensor] = None,
+                                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Full attention of q [B, H_q, D] over each sequence's seq_lens[b] tokens in 8-bit pages
+    (see include/loki.h). Returns out [B, H_q, D] of q's dtype."""
+    dev, B, H_q, H_kv, page_size, max_pages, n_pages, D, block = _check_attend_q8(
+        q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _cuda(q, out)
+        _expect(out, q.shape, q.dtype, "out")
+    with _on(dev):
+        ws = _ws(lib.dense_decode_paged_q8_workspace_size(B, H_q, H_kv, page_size, max_pages, D),
+                 dev, workspace)
+        check(lib.dense_decode_attention_paged_q8(
+            q.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block, block_table.data_ptr(), seq_lens.data_ptr(), B, H_q, H_kv,
+            page_size, max_pages, n_pages, D, scale, _dt(q), out.data_ptr(), ws.data_ptr(),
+            _ws_bytes(ws), _stream(dev)), "dense_decode_attention_paged_q8")
+    return out
+
+
+def loki_sparse_attention_paged_q8(q_rot: torch.Tensor, K8_pages: torch.Tensor,
+                                   V8_pages: torch.Tensor, k_scales: torch.Tensor,
+                                   v_scales: torch.Tensor, block_table: torch.Tensor,
+                                   seq_lens: torch.Tensor, selected_idx: torch.Tensor,
+                                   scale: float = 0.0, dtype: torch.dtype = torch.bfloat16,
+                                   out: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Exact attention of q_rot [B, H_q, D] fp32 over the tokens selected_idx [B, H_q, k] int32
+    names, in 8-bit pages. Returns out [B, H_q, D] of type `dtype` (or out's own)."""
+    dev, B, H_q, H_kv, page_size, max_pages, n_pages, D, block = _check_attend_q8(
+        q_rot, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace)
+    if q_rot.dtype != torch.float32:
+        raise TypeError("q_rot must be float32")
+    _cuda(q_rot, selected_idx)
+    if selected_idx.dim() != 3:
+        raise ValueError("selected_idx must be [B, H_q, k]")
+    k = selected_idx.shape[2]
+    _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
+    if out is None:
+        out = torch.empty((B, H_q, D), dtype=dtype, device=dev)
+    else:
+        _cuda(q_rot, out)
+        _expect(out, (B, H_q, D), out.dtype, "out")
+    with _on(dev):
+        ws = _ws(lib.loki_sparse_attention_paged_q8_workspace_size(B, H_q, H_kv, k, D), dev,
+                 workspace)
+        check(lib.loki_sparse_attention_paged_q8(
+            q_rot.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block, block_table.data_ptr(), seq_lens.data_ptr(),
+            selected_idx.data_ptr(), B, H_q, H_kv, page_size, max_pages, n_pages, D, k, scale,
+            _dt(out), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream(dev)),
+            "loki_sparse_attention_paged_q8")
+    return out
+
+
+def loki_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor, V8_pages: torch.Tensor,
+                                   k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                   Kt_lo_pages: torch.Tensor, P: torch.Tensor,
+                                   block_table: torch.Tensor, seq_lens: torch.Tensor, d: int,
+                                   k: int, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                                   selected_idx: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None
+                                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """loki_decode_attention_paged with keys and values in 8-bit pages (the plane in q's dtype).
+    Returns (out [B, H_q, D], selected_idx [B, H_q, k] int32, -1 padded)."""
+    dev, B, H_q, H_kv, page_size, max_pages, n_pages, D, block = _check_attend_q8(
+        q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace)
+    _cuda(q, Kt_lo_pages, P)
+    if Kt_lo_pages.dim() != 4:
+        raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
+    _expect(Kt_lo_pages, (n_pages, H_kv, page_size, Kt_lo_pages.shape[3]), q.dtype, "Kt_lo_pages")
+    _expect(P, (H_kv, D, D), torch.float32, "P")
+    if out is None:
+        out = torch.empty_like(q)
+    if selected_idx is None:
+        selected_idx = torch.empty((B, H_q, k), dtype=torch.int32, device=dev)
+    _cuda(q, out, selected_idx)
+    _expect(out, q.shape, q.dtype, "out")
+    _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
+    with _on(dev):
+        ws = _ws(loki_paged_q8_decode_workspace_size(B, H_q, H_kv, page_size, max_pages, D, d, k),
+                 dev, workspace)
+        check(lib.loki_decode_attention_paged_q8(
+            q.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block, Kt_lo_pages.data_ptr(), Kt_lo_pages.shape[3], P.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, H_q, H_kv, page_size, max_pages,
+            n_pages, D, d, k, scale, _dt(q), out.data_ptr(), selected_idx.data_ptr(),
+            ws.data_ptr(), _ws_bytes(ws), _stream(dev)), "loki_decode_attention_paged_q8")
+    return out, selected_idx
 
 
 def loki_decode_attention_fused(q: torch.Tensor, Kt_cache: torch.Tensor, V_cache: torch.Tensor,

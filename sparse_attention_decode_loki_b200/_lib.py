@@ -63,6 +63,37 @@ PROTOTYPES = {
     "loki_append_keys_paged": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_int, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                        c_int, c_int64, c_int, c_int, c_void_p]),
+    "loki_rope_table": (c_int, [c_void_p, c_int64, c_int, ctypes.c_double, ctypes.c_double,
+                                c_void_p]),
+    "loki_append_keys_paged_rope": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int,
+                                            c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                            c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int,
+                                            c_int, c_int, c_int, c_int, c_int64, c_int, c_int,
+                                            c_void_p]),
+    "loki_append_keys_paged_q8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int,
+                                          c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p,
+                                          c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                          c_int64, c_int, c_int, c_void_p]),
+    "dense_decode_paged_q8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "dense_decode_attention_paged_q8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                                c_int, c_void_p, c_void_p, c_int, c_int, c_int,
+                                                c_int, c_int, c_int64, c_int, c_float, c_int,
+                                                c_void_p, c_void_p, c_size_t, c_void_p]),
+    "loki_sparse_attention_paged_q8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int64,
+                                                                 c_int]),
+    "loki_sparse_attention_paged_q8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                               c_int, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                                               c_int, c_int, c_int, c_int64, c_int, c_int64,
+                                               c_float, c_int, c_void_p, c_void_p, c_size_t,
+                                               c_void_p]),
+    "loki_paged_q8_decode_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int,
+                                                       c_int, c_int64]),
+    "loki_decode_attention_paged_q8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                               c_int, c_void_p, c_int, c_void_p, c_void_p,
+                                               c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                               c_int64, c_int, c_int, c_int64, c_float, c_int,
+                                               c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "loki_project_query": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p,
                                    c_void_p]),
     "loki_score_lowdim": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int64, c_int64, c_int,

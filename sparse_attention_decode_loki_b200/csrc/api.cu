@@ -511,17 +511,24 @@ size_t loki_paged_decode_workspace_size(int B, int H_q, int H_kv, int page_size,
     return paged_ws(B, H_q, (int64_t)page_size * max_pages, D, k).total;
 }
 
-loki_status loki_decode_attention_paged(const void* q, const void* Kt_pages, const void* V_pages,
-                                        const void* Kt_lo_pages, int d_lo, const float* P,
-                                        const int32_t* block_table, const int32_t* seq_lens,
-                                        int B, int H_q, int H_kv, int page_size, int max_pages,
-                                        int64_t n_pages, int D, int d, int64_t k, float scale,
-                                        loki_dtype dt, void* out, int32_t* selected_idx,
-                                        void* ws, size_t ws_bytes, void* stream) {
-    g_last_error.clear();
-    LOKI_CHECK(check_dtype(dt));
-    LOKI_CHECK(check_heads(B, H_q, H_kv, D));
-    LOKI_CHECK(check_pages(page_size, max_pages, n_pages, H_kv));
+// The selection half of a paged decode: checks, the rotated queries (and
+// zeroed row counters), the lengths' work split, the paged scan and top-k per
+// row length. The attention over the selected tokens follows it.
+struct PagedPlan {
+    float* q_rot;
+    float* scores;
+    const int* lens;  // clamped lengths
+    void* dws;        // the decode workspace (layout w)
+    DecodeWs w;
+    size_t ws_total;  // bytes of ws the selection and the gather of dt pages take
+};
+
+static loki_status paged_select(const char* name, PagedPlan* p, const void* q,
+                                const void* Kt_lo_pages, int d_lo, const float* P,
+                                const int32_t* block_table, const int32_t* seq_lens, int B,
+                                int H_q, int H_kv, int page_size, int max_pages, int64_t n_pages,
+                                int D, int d, int64_t k, loki_dtype dt, int32_t* selected_idx,
+                                void* ws, size_t ws_bytes, size_t ws_need, void* stream) {
     LOKI_CHECK(check_plane(d_lo, D, dt));
     const int64_t S_cap = (int64_t)page_size * max_pages;
     LOKI_REQUIRE(d >= 1 && d <= d_lo, LOKI_ERR_INVALID_ARG, "d must be in [1, d_lo] (got %d)", d);
@@ -534,50 +541,72 @@ loki_status loki_decode_attention_paged(const void* q, const void* Kt_pages, con
     LOKI_REQUIRE(S_cap <= 262144, LOKI_ERR_UNSUPPORTED,
                  "paged decode selects from at most 262144 tokens per sequence");
     LOKI_PTR(q, 16);
-    LOKI_PTR(Kt_pages, 16);
-    LOKI_PTR(V_pages, 16);
     LOKI_PTR(Kt_lo_pages, 16);
     LOKI_PTR(P, 16);
     LOKI_PTR(block_table, 4);
     LOKI_PTR(seq_lens, 4);
-    LOKI_PTR(out, 16);
     LOKI_PTR(selected_idx, 4);
     LOKI_PTR(ws, 256);
-    const PagedWs pw = paged_ws(B, H_q, S_cap, D, k);
-    LOKI_REQUIRE(ws_bytes >= pw.total, LOKI_ERR_WORKSPACE_TOO_SMALL,
-                 "workspace %zu bytes < required %zu", ws_bytes, pw.total);
+    LOKI_REQUIRE(ws_bytes >= ws_need, LOKI_ERR_WORKSPACE_TOO_SMALL,
+                 "workspace %zu bytes < required %zu", ws_bytes, ws_need);
     const int grid = loki::paged_scan_grid();
     LOKI_REQUIRE(grid >= 1 && grid <= kPagedMaxGrid, LOKI_ERR_CUDA, "no usable current CUDA device");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const char* name = "loki_decode_attention_paged";
+    const PagedWs pw = paged_ws(B, H_q, S_cap, D, k);
     void* start_ws = at<char>(ws, pw.start);
-    void* dws = at<char>(ws, pw.dec);
-    const DecodeWs w = decode_ws(B, H_q, S_cap, D, k);
-    float* q_rot = at<float>(dws, w.q_rot);
-    float* scores = at<float>(dws, w.scores);
-    int* done = at<int>(dws, w.done);
+    p->dws = at<char>(ws, pw.dec);
+    p->w = decode_ws(B, H_q, S_cap, D, k);
+    p->q_rot = at<float>(p->dws, p->w.q_rot);
+    p->scores = at<float>(p->dws, p->w.scores);
+    p->lens = loki::paged_lens(start_ws, B);
+    p->ws_total = pw.total;
     const int rows = B * H_q;
-    // the rotated queries (and zeroed row counters), the lengths' work split,
-    // the paged scan, then top-k per row length and the paged gather
-    LOKI_CUDA(loki::launch_project_query(t, q, P, B, H_q, H_kv, D, q_rot, s, done, rows), name);
+    LOKI_CUDA(loki::launch_project_query(t, q, P, B, H_q, H_kv, D, p->q_rot, s,
+                                         at<int>(p->dws, p->w.done), rows),
+              name);
     LOKI_CUDA(loki::launch_paged_prefix(seq_lens, B, H_kv, S_cap, start_ws, grid, s), name);
-    LOKI_CUDA(loki::launch_score_paged(t, q_rot, Kt_lo_pages, d_lo, block_table, start_ws, B, H_q,
-                                       H_kv, page_size, max_pages, n_pages, S_cap, d, D, scores,
-                                       grid, s),
+    LOKI_CUDA(loki::launch_score_paged(t, p->q_rot, Kt_lo_pages, d_lo, block_table, start_ws, B,
+                                       H_q, H_kv, page_size, max_pages, n_pages, S_cap, d, D,
+                                       p->scores, grid, s),
               name);
-    const int* lens = loki::paged_lens(start_ws, B);
-    LOKI_CUDA(loki::launch_topk(scores, (int64_t)rows, S_cap, k, selected_idx, s, true, lens, H_q),
+    LOKI_CUDA(loki::launch_topk(p->scores, (int64_t)rows, S_cap, k, selected_idx, s, true, p->lens,
+                                H_q),
               name);
+    return LOKI_OK;
+}
+
+loki_status loki_decode_attention_paged(const void* q, const void* Kt_pages, const void* V_pages,
+                                        const void* Kt_lo_pages, int d_lo, const float* P,
+                                        const int32_t* block_table, const int32_t* seq_lens,
+                                        int B, int H_q, int H_kv, int page_size, int max_pages,
+                                        int64_t n_pages, int D, int d, int64_t k, float scale,
+                                        loki_dtype dt, void* out, int32_t* selected_idx,
+                                        void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    LOKI_CHECK(check_dtype(dt));
+    LOKI_CHECK(check_heads(B, H_q, H_kv, D));
+    LOKI_CHECK(check_pages(page_size, max_pages, n_pages, H_kv));
+    LOKI_PTR(Kt_pages, 16);
+    LOKI_PTR(V_pages, 16);
+    LOKI_PTR(out, 16);
+    const int64_t S_cap = (int64_t)page_size * max_pages;
+    const char* name = "loki_decode_attention_paged";
+    PagedPlan p;
+    LOKI_CHECK(paged_select(name, &p, q, Kt_lo_pages, d_lo, P, block_table, seq_lens, B, H_q, H_kv,
+                            page_size, max_pages, n_pages, D, d, k, dt, selected_idx, ws, ws_bytes,
+                            paged_ws(B, H_q, S_cap, D, k).total, stream));
     loki::PagedKV pg;
     pg.block_table = block_table;
     pg.page_size = page_size;
     pg.max_pages = max_pages;
     pg.n_pages = n_pages;
-    pg.lens = lens;
-    LOKI_CUDA(loki::launch_sparse_attention(t, q_rot, Kt_pages, V_pages, selected_idx, B, H_q, H_kv,
-                                            S_cap, S_cap, D, k, resolve_scale(scale, D), out,
-                                            at<float2>(dws, w.ml), at<float>(dws, w.acc), done, s,
-                                            true, pg, scores, d),
+    pg.lens = p.lens;
+    LOKI_CUDA(loki::launch_sparse_attention(to_dt(dt), p.q_rot, Kt_pages, V_pages, selected_idx, B,
+                                            H_q, H_kv, S_cap, S_cap, D, k, resolve_scale(scale, D),
+                                            out, at<float2>(p.dws, p.w.ml),
+                                            at<float>(p.dws, p.w.acc), at<int>(p.dws, p.w.done),
+                                            static_cast<cudaStream_t>(stream), true, pg, p.scores,
+                                            d),
               name);
     return LOKI_OK;
 }
@@ -613,6 +642,272 @@ loki_status loki_append_keys_paged(const void* K_new, const void* V_new, const f
                                   D, 0, 0, static_cast<cudaStream_t>(stream), nullptr, 0, false,
                                   &pg, positions),
               "loki_append_keys_paged");
+    return LOKI_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Paged appends with the rotary embedding, 8-bit pages
+
+loki_status loki_rope_table(float* table, int64_t n_pos, int rot_dim, double base,
+                            double pos_scale, void* stream) {
+    g_last_error.clear();
+    LOKI_REQUIRE(n_pos >= 1, LOKI_ERR_INVALID_ARG, "n_pos must be >= 1 (got %lld)", (long long)n_pos);
+    LOKI_REQUIRE(rot_dim >= 16 && rot_dim <= 128 && rot_dim % 16 == 0, LOKI_ERR_INVALID_ARG,
+                 "rot_dim must be a multiple of 16 in [16, 128] (got %d)", rot_dim);
+    LOKI_REQUIRE(base > 0 && isfinite(base) && isfinite(pos_scale), LOKI_ERR_INVALID_ARG,
+                 "base must be positive and, like pos_scale, finite");
+    LOKI_PTR(table, 16);
+    LOKI_CUDA(loki::launch_rope_table(table, n_pos, rot_dim, base, pos_scale,
+                                      static_cast<cudaStream_t>(stream)),
+              "loki_rope_table");
+    return LOKI_OK;
+}
+
+static loki_status check_block(int block, int page_size) {
+    LOKI_REQUIRE(block == 16 || block == 32 || block == 64 || block == 128, LOKI_ERR_INVALID_ARG,
+                 "block must be 16, 32, 64 or 128 tokens (got %d)", block);
+    LOKI_REQUIRE(page_size % block == 0, LOKI_ERR_INVALID_ARG,
+                 "page_size (%d) must be a multiple of block (%d)", page_size, block);
+    return LOKI_OK;
+}
+
+// What the two appends share: checks and the launch.
+static loki_status append_paged_impl(const char* name, const loki::AppendArgs& a, loki_dtype dt,
+                                     void* stream) {
+    LOKI_CHECK(check_dtype(dt));
+    LOKI_CHECK(check_heads(a.B, a.q != nullptr ? a.H_q : a.H_kv, a.H_kv, a.D));
+    LOKI_CHECK(check_pages(a.page_size, a.max_pages, a.n_pages, a.H_kv));
+    LOKI_REQUIRE(a.T >= 1, LOKI_ERR_INVALID_ARG, "T must be >= 1 (got %d)", a.T);
+    LOKI_PTR(a.K_new, 16);
+    LOKI_PTR(a.V_new, 16);
+    LOKI_PTR(a.K_pages, 16);
+    LOKI_PTR(a.V_pages, 16);
+    LOKI_PTR(a.block_table, 4);
+    LOKI_PTR(a.positions, 4);
+    if (a.P != nullptr) LOKI_PTR(a.P, 16);
+    if (a.new_lens != nullptr) LOKI_PTR(a.new_lens, 4);
+    if (a.rope != nullptr) {
+        LOKI_PTR(a.rope, 16);
+        LOKI_REQUIRE(a.n_pos >= 1, LOKI_ERR_INVALID_ARG, "n_pos must be >= 1");
+        LOKI_REQUIRE(a.rot_dim >= 16 && a.rot_dim <= a.D && a.rot_dim % 16 == 0,
+                     LOKI_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, D] (got %d)",
+                     a.rot_dim);
+    }
+    LOKI_REQUIRE((a.q != nullptr) == (a.q_out != nullptr), LOKI_ERR_INVALID_ARG,
+                 "q and q_out must be given together");
+    if (a.q != nullptr) {
+        LOKI_PTR(a.q, 16);
+        LOKI_PTR(a.q_out, 16);
+    }
+    if (a.plane != nullptr) {
+        LOKI_CHECK(check_plane(a.d_lo, a.D, dt));
+        LOKI_PTR(a.plane, 16);
+    }
+    LOKI_CUDA(loki::launch_append_paged(to_dt(dt), a, static_cast<cudaStream_t>(stream)), name);
+    return LOKI_OK;
+}
+
+loki_status loki_append_keys_paged_rope(
+    const void* K_new, const void* V_new, const float* P, const float* rope_table, int64_t n_pos,
+    int rot_dim, int interleaved, const void* q, void* q_out, int H_q, void* Kt_pages,
+    void* V_pages, void* Kt_lo_pages, int d_lo, const int32_t* block_table,
+    const int32_t* positions, const int32_t* new_lens, int B, int H_kv, int T, int page_size,
+    int max_pages, int64_t n_pages, int D, loki_dtype dt, void* stream) {
+    g_last_error.clear();
+    loki::AppendArgs a;
+    a.K_new = K_new;
+    a.V_new = V_new;
+    a.P = P;
+    a.rope = rope_table;
+    a.n_pos = n_pos;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved;
+    a.q = q;
+    a.q_out = q_out;
+    a.H_q = H_q;
+    a.K_pages = Kt_pages;
+    a.V_pages = V_pages;
+    a.plane = Kt_lo_pages;
+    a.d_lo = Kt_lo_pages != nullptr ? d_lo : 0;
+    a.block_table = block_table;
+    a.positions = positions;
+    a.new_lens = new_lens;
+    a.B = B;
+    a.H_kv = H_kv;
+    a.T = T;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.D = D;
+    return append_paged_impl("loki_append_keys_paged_rope", a, dt, stream);
+}
+
+loki_status loki_append_keys_paged_q8(
+    const void* K_new, const void* V_new, const float* P, const float* rope_table, int64_t n_pos,
+    int rot_dim, int interleaved, const void* q, void* q_out, int H_q, void* K8_pages,
+    void* V8_pages, float* k_scales, float* v_scales, int block, void* Kt_lo_pages, int d_lo,
+    const int32_t* block_table, const int32_t* positions, const int32_t* new_lens, int B, int H_kv,
+    int T, int page_size, int max_pages, int64_t n_pages, int D, loki_dtype dt, void* stream) {
+    g_last_error.clear();
+    LOKI_CHECK(check_block(block, page_size));
+    LOKI_PTR(k_scales, 4);
+    LOKI_PTR(v_scales, 4);
+    loki::AppendArgs a;
+    a.K_new = K_new;
+    a.V_new = V_new;
+    a.P = P;
+    a.rope = rope_table;
+    a.n_pos = n_pos;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved;
+    a.q = q;
+    a.q_out = q_out;
+    a.H_q = H_q;
+    a.K_pages = K8_pages;
+    a.V_pages = V8_pages;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.block = block;
+    a.plane = Kt_lo_pages;
+    a.d_lo = Kt_lo_pages != nullptr ? d_lo : 0;
+    a.block_table = block_table;
+    a.positions = positions;
+    a.new_lens = new_lens;
+    a.B = B;
+    a.H_kv = H_kv;
+    a.T = T;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.D = D;
+    return append_paged_impl("loki_append_keys_paged_q8", a, dt, stream);
+}
+
+size_t dense_decode_paged_q8_workspace_size(int B, int H_q, int H_kv, int page_size, int max_pages,
+                                            int D) {
+    if (B < 1 || H_q < 1 || H_kv < 1 || page_size < 1 || max_pages < 1 || D < 1) return 0;
+    return align_up(loki::dense_q8_ws_bytes(B, H_q, H_kv, (int64_t)page_size * max_pages, D));
+}
+
+size_t loki_sparse_attention_paged_q8_workspace_size(int B, int H_q, int H_kv, int64_t k, int D) {
+    if (B < 1 || H_q < 1 || H_kv < 1 || k < 1 || D < 1) return 0;
+    return align_up(loki::sparse_q8_ws_bytes(B, H_q, k, D));
+}
+
+// What the two attentions over 8-bit pages share: checks and the argument block.
+static loki_status attend_q8_args(loki::AttendQ8Args* a, const void* q, int q_f32, const void* K8,
+                                  const void* V8, const float* k_scales, const float* v_scales,
+                                  int block, const int32_t* block_table, const int32_t* seq_lens,
+                                  int B, int H_q, int H_kv, int page_size, int max_pages,
+                                  int64_t n_pages, int D, float scale, loki_dtype dt, void* out) {
+    LOKI_CHECK(check_dtype(dt));
+    LOKI_CHECK(check_heads(B, H_q, H_kv, D));
+    LOKI_CHECK(check_pages(page_size, max_pages, n_pages, H_kv));
+    LOKI_CHECK(check_block(block, page_size));
+    LOKI_PTR(q, 16);
+    LOKI_PTR(K8, 16);
+    LOKI_PTR(V8, 16);
+    LOKI_PTR(k_scales, 4);
+    LOKI_PTR(v_scales, 4);
+    LOKI_PTR(block_table, 4);
+    LOKI_PTR(seq_lens, 4);
+    LOKI_PTR(out, 16);
+    a->q = q;
+    a->q_f32 = q_f32;
+    a->K_pages = static_cast<const uint8_t*>(K8);
+    a->V_pages = static_cast<const uint8_t*>(V8);
+    a->k_scales = k_scales;
+    a->v_scales = v_scales;
+    a->block = block;
+    a->block_table = block_table;
+    a->seq_lens = seq_lens;
+    a->B = B;
+    a->H_q = H_q;
+    a->H_kv = H_kv;
+    a->page_size = page_size;
+    a->max_pages = max_pages;
+    a->n_pages = n_pages;
+    a->D = D;
+    a->scale_log2 = resolve_scale(scale, D) * 1.4426950408889634f;
+    a->out = out;
+    return LOKI_OK;
+}
+
+loki_status dense_decode_attention_paged_q8(
+    const void* q, const void* K8_pages, const void* V8_pages, const float* k_scales,
+    const float* v_scales, int block, const int32_t* block_table, const int32_t* seq_lens, int B,
+    int H_q, int H_kv, int page_size, int max_pages, int64_t n_pages, int D, float scale,
+    loki_dtype dt, void* out, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    loki::AttendQ8Args a;
+    LOKI_CHECK(attend_q8_args(&a, q, dt == LOKI_DTYPE_F32, K8_pages, V8_pages, k_scales, v_scales,
+                              block, block_table, seq_lens, B, H_q, H_kv, page_size, max_pages,
+                              n_pages, D, scale, dt, out));
+    LOKI_PTR(ws, 256);
+    const size_t need = dense_decode_paged_q8_workspace_size(B, H_q, H_kv, page_size, max_pages, D);
+    LOKI_REQUIRE(ws_bytes >= need, LOKI_ERR_WORKSPACE_TOO_SMALL,
+                 "workspace %zu bytes < required %zu", ws_bytes, need);
+    a.ws = ws;
+    LOKI_CUDA(loki::launch_attend_q8(to_dt(dt), a, static_cast<cudaStream_t>(stream)),
+              "dense_decode_attention_paged_q8");
+    return LOKI_OK;
+}
+
+loki_status loki_sparse_attention_paged_q8(
+    const float* q_rot, const void* K8_pages, const void* V8_pages, const float* k_scales,
+    const float* v_scales, int block, const int32_t* block_table, const int32_t* seq_lens,
+    const int32_t* selected_idx, int B, int H_q, int H_kv, int page_size, int max_pages,
+    int64_t n_pages, int D, int64_t k, float scale, loki_dtype dt, void* out, void* ws,
+    size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    loki::AttendQ8Args a;
+    LOKI_CHECK(attend_q8_args(&a, q_rot, 1, K8_pages, V8_pages, k_scales, v_scales, block,
+                              block_table, seq_lens, B, H_q, H_kv, page_size, max_pages, n_pages, D,
+                              scale, dt, out));
+    LOKI_REQUIRE(k >= 1 && k <= kMaxS, LOKI_ERR_INVALID_ARG, "k must be in [1, 2^31)");
+    LOKI_PTR(selected_idx, 4);
+    LOKI_PTR(ws, 256);
+    const size_t need = loki_sparse_attention_paged_q8_workspace_size(B, H_q, H_kv, k, D);
+    LOKI_REQUIRE(ws_bytes >= need, LOKI_ERR_WORKSPACE_TOO_SMALL,
+                 "workspace %zu bytes < required %zu", ws_bytes, need);
+    a.idx = selected_idx;
+    a.k = k;
+    a.ws = ws;
+    LOKI_CUDA(loki::launch_attend_q8(to_dt(dt), a, static_cast<cudaStream_t>(stream)),
+              "loki_sparse_attention_paged_q8");
+    return LOKI_OK;
+}
+
+size_t loki_paged_q8_decode_workspace_size(int B, int H_q, int H_kv, int page_size, int max_pages,
+                                           int D, int d, int64_t k) {
+    const size_t base = loki_paged_decode_workspace_size(B, H_q, H_kv, page_size, max_pages, D, d, k);
+    if (base == 0 || H_kv < 1) return 0;
+    return align_up(base) + loki_sparse_attention_paged_q8_workspace_size(B, H_q, H_kv, k, D);
+}
+
+loki_status loki_decode_attention_paged_q8(
+    const void* q, const void* K8_pages, const void* V8_pages, const float* k_scales,
+    const float* v_scales, int block, const void* Kt_lo_pages, int d_lo, const float* P,
+    const int32_t* block_table, const int32_t* seq_lens, int B, int H_q, int H_kv, int page_size,
+    int max_pages, int64_t n_pages, int D, int d, int64_t k, float scale, loki_dtype dt, void* out,
+    int32_t* selected_idx, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    loki::AttendQ8Args a;
+    LOKI_CHECK(attend_q8_args(&a, q, 1, K8_pages, V8_pages, k_scales, v_scales, block, block_table,
+                              seq_lens, B, H_q, H_kv, page_size, max_pages, n_pages, D, scale, dt,
+                              out));
+    const char* name = "loki_decode_attention_paged_q8";
+    PagedPlan p;
+    LOKI_CHECK(paged_select(name, &p, q, Kt_lo_pages, d_lo, P, block_table, seq_lens, B, H_q, H_kv,
+                            page_size, max_pages, n_pages, D, d, k, dt, selected_idx, ws, ws_bytes,
+                            loki_paged_q8_decode_workspace_size(B, H_q, H_kv, page_size, max_pages,
+                                                                D, d, k),
+                            stream));
+    a.q = p.q_rot;
+    a.idx = selected_idx;
+    a.k = k;
+    a.ws = at<char>(ws, align_up(p.ws_total));
+    LOKI_CUDA(loki::launch_attend_q8(to_dt(dt), a, static_cast<cudaStream_t>(stream)), name);
     return LOKI_OK;
 }
 

@@ -173,6 +173,59 @@ cudaError_t launch_pca_attention(Dt dt, const float* q_rot, const void* Klo, int
                                  int D, float scale, void* out, float2* part_ml, float* part_acc,
                                  cudaStream_t s);
 
+// ---- paged appends with the rotary embedding, 8-bit pages -------------------
+struct AppendArgs {
+    const void* K_new = nullptr;
+    const void* V_new = nullptr;
+    const float* P = nullptr;     // may be null: no basis
+    const float* rope = nullptr;  // [n_pos, rot_dim]; may be null: no rotary embedding
+    int64_t n_pos = 0;
+    int rot_dim = 0, interleaved = 0;
+    const void* q = nullptr;  // [B, H_q, T, D], may be null
+    void* q_out = nullptr;
+    void* K_pages = nullptr;
+    void* V_pages = nullptr;
+    float* k_scales = nullptr;  // 8-bit pages only (block > 0)
+    float* v_scales = nullptr;
+    void* plane = nullptr;  // may be null
+    int d_lo = 0, block = 0;
+    const int* block_table = nullptr;
+    const int* positions = nullptr;
+    const int* new_lens = nullptr;  // may be null: all T tokens
+    int B = 0, H_q = 0, H_kv = 0, T = 0, page_size = 0, max_pages = 0, D = 0;
+    int64_t n_pages = 0;
+    // set by the launcher
+    int tile = 0;
+    int64_t kv_items = 0, items = 0;
+    int* err = nullptr;
+};
+cudaError_t launch_append_paged(Dt dt, AppendArgs a, cudaStream_t s);
+cudaError_t launch_rope_table(float* table, int64_t n_pos, int rot_dim, double base,
+                              double pos_scale, cudaStream_t s);
+
+struct AttendQ8Args {
+    const void* q = nullptr;  // [B, H_q, D] fp32 (q_f32) or bf16
+    int q_f32 = 0;
+    const uint8_t* K_pages = nullptr;
+    const uint8_t* V_pages = nullptr;
+    const float* k_scales = nullptr;
+    const float* v_scales = nullptr;
+    const int* block_table = nullptr;
+    const int* seq_lens = nullptr;
+    const int32_t* idx = nullptr;  // [B, H_q, k]; null: all tokens
+    int64_t k = 0;
+    int B = 0, H_q = 0, H_kv = 0, page_size = 0, max_pages = 0, block = 0, D = 0;
+    int64_t n_pages = 0;
+    float scale_log2 = 0.f;
+    void* out = nullptr;
+    void* ws = nullptr;
+    int* err = nullptr;  // set by the launcher
+};
+// bytes of a.ws
+size_t dense_q8_ws_bytes(int B, int H_q, int H_kv, int64_t S_cap, int D);
+size_t sparse_q8_ws_bytes(int B, int H_q, int64_t k, int D);
+cudaError_t launch_attend_q8(Dt out_dt, AttendQ8Args a, cudaStream_t s);
+
 // ---- supporting subsystems -----------------------------------------------
 // Kt_lo (may be null): [B, H_kv, S_max, d_lo] plane that also receives the
 // first d_lo rotated columns of each appended key.
