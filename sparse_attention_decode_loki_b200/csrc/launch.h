@@ -219,7 +219,11 @@ struct AttendQ8Args {
     float scale_log2 = 0.f;
     void* out = nullptr;
     void* ws = nullptr;
-    int* err = nullptr;  // set by the launcher
+    // set by the launcher
+    int page_log2 = 0;  // -1: not a power of two
+    int block_log2 = 0, warps = 0;
+    int64_t slots = 0;
+    int* err = nullptr;
 };
 // bytes of a.ws
 size_t dense_q8_ws_bytes(int B, int H_q, int H_kv, int64_t S_cap, int D);
