@@ -194,12 +194,16 @@ struct AppendArgs {
     const int* new_lens = nullptr;  // may be null: all T tokens
     int B = 0, H_q = 0, H_kv = 0, T = 0, page_size = 0, max_pages = 0, D = 0;
     int64_t n_pages = 0;
-    // set by the launcher
-    int tile = 0;
-    int64_t kv_items = 0, items = 0;
+    // set by the launchers
+    int page_log2 = 0;  // -1: not a power of two
+    int block_log2 = 0, group = 0, kv_ctas = 0;
+    int64_t key_tasks = 0, value_tasks = 0, query_tasks = 0;
     int* err = nullptr;
 };
 cudaError_t launch_append_paged(Dt dt, AppendArgs a, cudaStream_t s);
+// the keys' part of a longer append with a basis; the values' and queries'
+// stream runs as its programmatic dependent
+cudaError_t launch_append_basis(Dt dt, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_rope_table(float* table, int64_t n_pos, int rot_dim, double base,
                               double pos_scale, cudaStream_t s);
 
