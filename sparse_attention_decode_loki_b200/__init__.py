@@ -13,7 +13,7 @@ top k are kept, and exact softmax attention runs over those k tokens only.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -68,12 +68,16 @@ def _cuda(*ts: torch.Tensor) -> torch.device:
 
 
 def _expect(t: torch.Tensor, shape, dtype, name: str) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {list(shape)} (got {t.dtype} {list(t.shape)})")
 
 
+# The raw handle by itself: 0.1 us, where the Stream object around it takes 2.2 us.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 def _ws(nbytes: int, dev: torch.device, ws: Optional[torch.Tensor]) -> torch.Tensor:
@@ -363,11 +367,28 @@ def loki_append_keys_paged(K_new: torch.Tensor, V_new: torch.Tensor, P: torch.Te
 # paged appends with the rotary embedding, 8-bit pages
 # ---------------------------------------------------------------------------
 
-def _on(dev: torch.device):
-    """Makes the tensors' device the current one for the library's launches."""
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _place(*ts: torch.Tensor) -> int:
+    """The CUDA device index that contiguous tensors share (_cuda's checks, without device objects:
+    a decode step's calls are short enough for the host's side to count)."""
+    i = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != i or not t.is_contiguous():
+            _cuda(*ts)
+    if i < 0:
+        _cuda(*ts)
+    return i
+
+
+def _launch(name: str, i: int, args: tuple) -> None:
+    """Calls the library's `name` on device i's current stream, with i as the current device."""
+    f = getattr(lib, name)
+    if torch.cuda.current_device() == i:
+        status = f(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = f(*args, _raw_stream(i))
+    if status != 0:
+        check(status, name)
 
 
 def loki_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, pos_scale: float = 1.0,
@@ -378,44 +399,45 @@ def loki_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, pos_scale: 
     if table is None:
         table = torch.empty((n_pos, rot_dim), dtype=torch.float32,
                             device="cuda" if device is None else device)
-    dev = _cuda(table)
+    i = _place(table)
     _expect(table, (n_pos, rot_dim), torch.float32, "table")
-    with _on(dev):
-        check(lib.loki_rope_table(table.data_ptr(), n_pos, rot_dim, base, pos_scale, _stream(dev)),
-              "loki_rope_table")
+    _launch("loki_rope_table", i, (table.data_ptr(), n_pos, rot_dim, base, pos_scale))
     return table
 
 
 def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rope_table, plane,
-                  new_lens, q, q_out):
-    """What the two rotary appends share: (device, shapes, q_out, the C arguments around the pages)."""
-    ts = [K_new, V_new, K_pages, V_pages, block_table, positions]
-    for t in (P, rope_table, plane, new_lens, q, q_out):
-        if t is not None:
-            ts.append(t)
-    dev = _cuda(*ts)
-    if K_new.dim() != 4 or K_pages.dim() != 4 or block_table.dim() != 2:
+                  new_lens, q, q_out, *scales):
+    """What the two rotary appends share: (device index, H_q, q_out, the C arguments around the pages)."""
+    i = _place(K_new, V_new, K_pages, V_pages, block_table, positions, *scales,
+               *[t for t in (P, rope_table, plane, new_lens, q, q_out) if t is not None])
+    ks, ps, bs, dtype = K_new.shape, K_pages.shape, block_table.shape, K_new.dtype
+    if len(ks) != 4 or len(ps) != 4 or len(bs) != 2:
         raise ValueError("K_new [B, H_kv, T, D], pages [n_pages, H_kv, page_size, D] and "
                          "block_table [B, max_pages] expected")
-    B, H_kv, T, D = K_new.shape
-    n_pages, Hp, page_size, Dp = K_pages.shape
-    if (V_new.shape != K_new.shape or V_pages.shape != K_pages.shape or Hp != H_kv or Dp != D
-            or block_table.shape[0] != B or tuple(positions.shape) != (B,)):
+    B, H_kv, T, D = ks
+    n_pages, Hp, page_size, Dp = ps
+    if (V_new.shape != ks or V_pages.shape != ps or Hp != H_kv or Dp != D or bs[0] != B
+            or positions.shape != (B,)):
         raise ValueError("K_new, V_new [B, H_kv, T, D], the pages, block_table [B, max_pages] and "
                          "positions [B] disagree")
     if block_table.dtype != torch.int32 or positions.dtype != torch.int32:
         raise TypeError("block_table and positions must be int32")
     dt = _dt(K_new)
-    if V_new.dtype != K_new.dtype or V_pages.dtype != K_pages.dtype:
+    if V_new.dtype != dtype or V_pages.dtype != K_pages.dtype:
         raise TypeError("K_new and V_new, and the two page pools, must share a dtype")
     if P is not None:
         _expect(P, (H_kv, D, D), torch.float32, "P")
-    if rope_table is not None and (rope_table.dim() != 2 or rope_table.dtype != torch.float32):
-        raise ValueError("rope_table must be float32 [n_pos, rot_dim]")
+    table = (None, 0, 0)
+    if rope_table is not None:
+        if rope_table.dim() != 2 or rope_table.dtype != torch.float32:
+            raise ValueError("rope_table must be float32 [n_pos, rot_dim]")
+        table = (rope_table.data_ptr(), *rope_table.shape)
+    d_lo = 0
     if plane is not None:
         if plane.dim() != 4:
             raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
-        _expect(plane, (n_pages, H_kv, page_size, plane.shape[3]), K_new.dtype, "Kt_lo_pages")
+        d_lo = plane.shape[3]
+        _expect(plane, (n_pages, H_kv, page_size, d_lo), dtype, "Kt_lo_pages")
     if new_lens is not None:
         _expect(new_lens, (B,), torch.int32, "new_lens")
     H_q = H_kv
@@ -423,21 +445,18 @@ def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rop
         if q.dim() != 4:
             raise ValueError("q must be [B, H_q, T, D]")
         H_q = q.shape[1]
-        _expect(q, (B, H_q, T, D), K_new.dtype, "q")
+        _expect(q, (B, H_q, T, D), dtype, "q")
         if q_out is None:
             q_out = torch.empty_like(q)
         else:
             _expect(q_out, q.shape, q.dtype, "q_out")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    front = (K_new.data_ptr(), V_new.data_ptr(), None if P is None else P.data_ptr(),
-             *((None, 0, 0) if rope_table is None else
-               (rope_table.data_ptr(), rope_table.shape[0], rope_table.shape[1])))
-    back = (None if plane is None else plane.data_ptr(), 0 if plane is None else plane.shape[3],
-            block_table.data_ptr(), positions.data_ptr(),
-            None if new_lens is None else new_lens.data_ptr(), B, H_kv, T, page_size,
-            block_table.shape[1], n_pages, D, dt)
-    return dev, H_q, q_out, front, back
+    front = (K_new.data_ptr(), V_new.data_ptr(), None if P is None else P.data_ptr(), *table)
+    back = (None if plane is None else plane.data_ptr(), d_lo, block_table.data_ptr(),
+            positions.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, H_kv, T,
+            page_size, bs[1], n_pages, D, dt)
+    return i, H_q, q_out, front, back
 
 
 def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
@@ -453,17 +472,13 @@ def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Opt
     and turn the queries q [B, H_q, T, D] by the same angles; returns q_out (None without q).
     P None: no basis; rope_table None: no rotary embedding; new_lens [B] int32: only the first
     new_lens[b] tokens (see include/loki.h)."""
-    dev, H_q, q_out, front, back = _check_append(K_new, V_new, P, Kt_pages, V_pages, block_table,
-                                                 positions, rope_table, Kt_lo_pages, new_lens, q,
-                                                 q_out)
+    i, H_q, q_out, front, back = _check_append(K_new, V_new, P, Kt_pages, V_pages, block_table,
+                                               positions, rope_table, Kt_lo_pages, new_lens, q, q_out)
     if Kt_pages.dtype != K_new.dtype:
         raise TypeError("K_new and the pages must share a dtype")
-    with _on(dev):
-        check(lib.loki_append_keys_paged_rope(*front, int(interleaved),
-                                              None if q is None else q.data_ptr(),
-                                              None if q is None else q_out.data_ptr(), H_q,
-                                              Kt_pages.data_ptr(), V_pages.data_ptr(), *back,
-                                              _stream(dev)), "loki_append_keys_paged_rope")
+    _launch("loki_append_keys_paged_rope", i,
+            (*front, int(interleaved), None if q is None else q.data_ptr(),
+             None if q is None else q_out.data_ptr(), H_q, Kt_pages.data_ptr(), V_pages.data_ptr(), *back))
     return q_out
 
 
@@ -471,11 +486,12 @@ def _check_q8(K8_pages, V8_pages, k_scales, v_scales):
     """(block) of 8-bit pages and their scales."""
     if K8_pages.dtype != torch.float8_e4m3fn or V8_pages.dtype != torch.float8_e4m3fn:
         raise TypeError("8-bit pages must be torch.float8_e4m3fn")
-    if K8_pages.dim() != 4 or V8_pages.shape != K8_pages.shape or k_scales.dim() != 3:
+    ps, ss = K8_pages.shape, k_scales.shape
+    if len(ps) != 4 or V8_pages.shape != ps or len(ss) != 3:
         raise ValueError("pages [n_pages, H_kv, page_size, D] and scales [n_pages, H_kv, "
                          "page_size / block] expected")
-    n_pages, H_kv, page_size, _ = K8_pages.shape
-    nb = k_scales.shape[2]
+    n_pages, H_kv, page_size, _ = ps
+    nb = ss[2]
     if nb < 1 or page_size % nb:
         raise ValueError("page_size must be a multiple of the scales' blocks per page")
     _expect(k_scales, (n_pages, H_kv, nb), torch.float32, "k_scales")
@@ -495,17 +511,13 @@ def loki_append_keys_paged_q8(K_new: torch.Tensor, V_new: torch.Tensor, P: Optio
     """loki_append_keys_paged_rope into 8-bit pages: e4m3 codes [n_pages, H_kv, page_size, D]
     (torch.float8_e4m3fn) with fp32 scales [n_pages, H_kv, page_size / block], powers of two."""
     block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
-    dev, H_q, q_out, front, back = _check_append(K_new, V_new, P, K8_pages, V8_pages, block_table,
-                                                 positions, rope_table, Kt_lo_pages, new_lens, q,
-                                                 q_out)
-    _cuda(K_new, k_scales, v_scales)
-    with _on(dev):
-        check(lib.loki_append_keys_paged_q8(*front, int(interleaved),
-                                            None if q is None else q.data_ptr(),
-                                            None if q is None else q_out.data_ptr(), H_q,
-                                            K8_pages.data_ptr(), V8_pages.data_ptr(),
-                                            k_scales.data_ptr(), v_scales.data_ptr(), block, *back,
-                                            _stream(dev)), "loki_append_keys_paged_q8")
+    i, H_q, q_out, front, back = _check_append(K_new, V_new, P, K8_pages, V8_pages, block_table,
+                                               positions, rope_table, Kt_lo_pages, new_lens, q, q_out,
+                                               k_scales, v_scales)
+    _launch("loki_append_keys_paged_q8", i,
+            (*front, int(interleaved), None if q is None else q.data_ptr(),
+             None if q is None else q_out.data_ptr(), H_q, K8_pages.data_ptr(), V8_pages.data_ptr(),
+             k_scales.data_ptr(), v_scales.data_ptr(), block, *back))
     return q_out
 
 
@@ -524,20 +536,29 @@ def loki_paged_q8_decode_workspace_size(B: int, H_q: int, H_kv: int, page_size: 
     return int(lib.loki_paged_q8_decode_workspace_size(B, H_q, H_kv, page_size, max_pages, D, d, k))
 
 
-def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace):
-    """What the attentions over 8-bit pages share: (device, sizes of the C call)."""
+def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, *more):
+    """What the attentions over 8-bit pages share: (device index, the sizes B, H_q, H_kv, page_size,
+    max_pages, n_pages, D of the C calls, the C arguments in front of their own)."""
     block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
-    dev = _cuda(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens,
-                *(() if workspace is None else (workspace,)))
+    i = _place(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens,
+               *[t for t in more if t is not None])
     n_pages, H_kv, page_size, D = K8_pages.shape
-    if q.dim() != 3 or block_table.dim() != 2:
+    qs, bs = q.shape, block_table.shape
+    if len(qs) != 3 or len(bs) != 2:
         raise ValueError("q [B, H_q, D] and block_table [B, max_pages] expected")
-    B, H_q, Dq = q.shape
-    if Dq != D or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+    B, H_q, Dq = qs
+    if Dq != D or bs[0] != B or seq_lens.shape != (B,):
         raise ValueError("q [B, H_q, D], block_table [B, max_pages], seq_lens [B] disagree")
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_table and seq_lens must be int32")
-    return dev, B, H_q, H_kv, page_size, block_table.shape[1], n_pages, D, block
+    front = (q.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
+             v_scales.data_ptr(), block)
+    return i, (B, H_q, H_kv, page_size, bs[1], n_pages, D), front
+
+
+_dense_q8_ws = functools.lru_cache(maxsize=1024)(dense_decode_paged_q8_workspace_size)
+_sparse_q8_ws = functools.lru_cache(maxsize=1024)(loki_sparse_attention_paged_q8_workspace_size)
+_decode_q8_ws = functools.lru_cache(maxsize=1024)(loki_paged_q8_decode_workspace_size)
 
 
 def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
@@ -548,21 +569,17 @@ def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
                                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Full attention of q [B, H_q, D] over each sequence's seq_lens[b] tokens in 8-bit pages
     (see include/loki.h). Returns out [B, H_q, D] of q's dtype."""
-    dev, B, H_q, H_kv, page_size, max_pages, n_pages, D, block = _check_attend_q8(
-        q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace)
+    i, sizes, front = _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table,
+                                       seq_lens, out, workspace)
+    B, H_q, H_kv, page_size, max_pages, _, D = sizes
     if out is None:
         out = torch.empty_like(q)
     else:
-        _cuda(q, out)
         _expect(out, q.shape, q.dtype, "out")
-    with _on(dev):
-        ws = _ws(lib.dense_decode_paged_q8_workspace_size(B, H_q, H_kv, page_size, max_pages, D),
-                 dev, workspace)
-        check(lib.dense_decode_attention_paged_q8(
-            q.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block, block_table.data_ptr(), seq_lens.data_ptr(), B, H_q, H_kv,
-            page_size, max_pages, n_pages, D, scale, _dt(q), out.data_ptr(), ws.data_ptr(),
-            _ws_bytes(ws), _stream(dev)), "dense_decode_attention_paged_q8")
+    ws = _ws(_dense_q8_ws(B, H_q, H_kv, page_size, max_pages, D), q.device, workspace)
+    _launch("dense_decode_attention_paged_q8", i,
+            (*front, block_table.data_ptr(), seq_lens.data_ptr(), *sizes, scale, _dt(q),
+             out.data_ptr(), ws.data_ptr(), _ws_bytes(ws)))
     return out
 
 
@@ -575,29 +592,23 @@ def loki_sparse_attention_paged_q8(q_rot: torch.Tensor, K8_pages: torch.Tensor,
                                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Exact attention of q_rot [B, H_q, D] fp32 over the tokens selected_idx [B, H_q, k] int32
     names, in 8-bit pages. Returns out [B, H_q, D] of type `dtype` (or out's own)."""
-    dev, B, H_q, H_kv, page_size, max_pages, n_pages, D, block = _check_attend_q8(
-        q_rot, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace)
+    i, sizes, front = _check_attend_q8(q_rot, K8_pages, V8_pages, k_scales, v_scales, block_table,
+                                       seq_lens, selected_idx, out, workspace)
+    B, H_q, H_kv, _, _, _, D = sizes
     if q_rot.dtype != torch.float32:
         raise TypeError("q_rot must be float32")
-    _cuda(q_rot, selected_idx)
     if selected_idx.dim() != 3:
         raise ValueError("selected_idx must be [B, H_q, k]")
     k = selected_idx.shape[2]
     _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
     if out is None:
-        out = torch.empty((B, H_q, D), dtype=dtype, device=dev)
+        out = torch.empty((B, H_q, D), dtype=dtype, device=q_rot.device)
     else:
-        _cuda(q_rot, out)
         _expect(out, (B, H_q, D), out.dtype, "out")
-    with _on(dev):
-        ws = _ws(lib.loki_sparse_attention_paged_q8_workspace_size(B, H_q, H_kv, k, D), dev,
-                 workspace)
-        check(lib.loki_sparse_attention_paged_q8(
-            q_rot.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block, block_table.data_ptr(), seq_lens.data_ptr(),
-            selected_idx.data_ptr(), B, H_q, H_kv, page_size, max_pages, n_pages, D, k, scale,
-            _dt(out), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws), _stream(dev)),
-            "loki_sparse_attention_paged_q8")
+    ws = _ws(_sparse_q8_ws(B, H_q, H_kv, k, D), q_rot.device, workspace)
+    _launch("loki_sparse_attention_paged_q8", i,
+            (*front, block_table.data_ptr(), seq_lens.data_ptr(), selected_idx.data_ptr(), *sizes, k,
+             scale, _dt(out), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws)))
     return out
 
 
@@ -611,29 +622,25 @@ def loki_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor, V8_p
                                    ) -> Tuple[torch.Tensor, torch.Tensor]:
     """loki_decode_attention_paged with keys and values in 8-bit pages (the plane in q's dtype).
     Returns (out [B, H_q, D], selected_idx [B, H_q, k] int32, -1 padded)."""
-    dev, B, H_q, H_kv, page_size, max_pages, n_pages, D, block = _check_attend_q8(
-        q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, workspace)
-    _cuda(q, Kt_lo_pages, P)
+    i, sizes, front = _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table,
+                                       seq_lens, Kt_lo_pages, P, out, selected_idx, workspace)
+    B, H_q, H_kv, page_size, max_pages, n_pages, D = sizes
     if Kt_lo_pages.dim() != 4:
         raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
-    _expect(Kt_lo_pages, (n_pages, H_kv, page_size, Kt_lo_pages.shape[3]), q.dtype, "Kt_lo_pages")
+    d_lo = Kt_lo_pages.shape[3]
+    _expect(Kt_lo_pages, (n_pages, H_kv, page_size, d_lo), q.dtype, "Kt_lo_pages")
     _expect(P, (H_kv, D, D), torch.float32, "P")
     if out is None:
         out = torch.empty_like(q)
     if selected_idx is None:
-        selected_idx = torch.empty((B, H_q, k), dtype=torch.int32, device=dev)
-    _cuda(q, out, selected_idx)
+        selected_idx = torch.empty((B, H_q, k), dtype=torch.int32, device=q.device)
     _expect(out, q.shape, q.dtype, "out")
     _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
-    with _on(dev):
-        ws = _ws(loki_paged_q8_decode_workspace_size(B, H_q, H_kv, page_size, max_pages, D, d, k),
-                 dev, workspace)
-        check(lib.loki_decode_attention_paged_q8(
-            q.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block, Kt_lo_pages.data_ptr(), Kt_lo_pages.shape[3], P.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), B, H_q, H_kv, page_size, max_pages,
-            n_pages, D, d, k, scale, _dt(q), out.data_ptr(), selected_idx.data_ptr(),
-            ws.data_ptr(), _ws_bytes(ws), _stream(dev)), "loki_decode_attention_paged_q8")
+    ws = _ws(_decode_q8_ws(B, H_q, H_kv, page_size, max_pages, D, d, k), q.device, workspace)
+    _launch("loki_decode_attention_paged_q8", i,
+            (*front, Kt_lo_pages.data_ptr(), d_lo, P.data_ptr(), block_table.data_ptr(),
+             seq_lens.data_ptr(), *sizes, d, k, scale, _dt(q), out.data_ptr(),
+             selected_idx.data_ptr(), ws.data_ptr(), _ws_bytes(ws)))
     return out, selected_idx
 
 
