@@ -22,16 +22,30 @@
 // instruction has room for four heads; five to eight take two. (8-bit operands
 // would halve the instructions, but carry four bits of a query at a time.)
 //
-// Softmax in base 2, in fp32, with its maximum taken per tile: the tile's
-// weights are relative to its own maximum, and its product joins the running
-// sums with one fp32 factor that also carries the values' scale. So scales far
-// apart between blocks cost no precision.
+// Softmax in base 2, in fp32, against references that move rarely: a head's
+// weights are u = 2^(x - m) for the sum and w = u s_V 2^-E for the product; m
+// and the whole number E are raised (and the sums scaled down) only when a
+// score lies 8 above m or a weight would pass 2^15, fp16's range. So a tile
+// costs one warp vote instead of a maximum over its lanes, and the product
+// stays in the tensor cores' accumulators from tile to tile. E is set so that
+// the largest weight so far is 1/2 or more: a weight's rounding, 2^-22 of
+// itself or 2^-25, is 2^-24 of the largest weighted value at most, whatever
+// the scales of the other blocks.
+//
+// A warp keeps kStages tiles in a ring of its own in shared memory, two of
+// them on their way (128 KB in flight per SM): dense tiles, 16 rows of one
+// page, come as two bulk copies; selected tokens as cp.async, every lane
+// fetching and reading back its own fragments.
 //
 // The tiles of all (sequence, KV head) units - of all (sequence, query head)
 // rows, when tokens are selected - are laid end to end and dealt to the
 // resident warps in equal runs. A warp that owns a whole unit writes its
 // output, others leave partials (fp32 max, sum, D columns per head) that
-// k_q8_combine merges in a fixed order.
+// k_q8_combine merges in a fixed order. Where that would leave a warp only a
+// few tiles, latency counts, and one kernel does it all: a cluster of CTAs
+// takes a unit, its warps a run of tiles each, and the partials meet in
+// shared memory, the CTAs' through distributed shared memory.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "launch.h"
@@ -40,10 +54,16 @@
 
 namespace loki {
 
+namespace cg = cooperative_groups;
+
 constexpr int kQ8Threads = 128;
+constexpr int kClThreads = 256;  // of the cluster kernels
+constexpr int kStages = 3;
+constexpr int kClusterTiles = 8;  // the most tiles a warp of theirs takes
 constexpr int kQ8MaxWarps = 148 * 16;  // workspace is laid out for at most this many
 constexpr int kTile = 16;
 constexpr uint32_t kNoRow = 0xffffffffu;
+constexpr float kLeast = -3.402823466e38f;  // below every score
 
 // D[16x8] += A[16x16] B[16x8], fp16 in, fp32 out
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -65,89 +85,106 @@ __device__ __forceinline__ uint32_t f16_part(float x, float y, bool rest) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint2 ld_stream8(const void* p) {
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
+// N bytes (4, 8 or 16) to shared memory, zeros when !on
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
+    const int n = on ? N : 0;
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(N), "r"(n)
+                     : "memory");
 }
-__device__ __forceinline__ uint32_t ld_stream4(const void* p) {
-    uint32_t r;
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Lane (gid = lane / 4, tig = lane % 4) holds of a tile
+// A tile in shared memory. Lane (gid = lane / 4, tig = lane % 4) reads
 //   keys:   tokens tk = 4 (gid / 2) + gid % 2 and tk + 2, the columns
 //           key_col(w, tig) .. + 3 as word w;
 //   values: tokens 4 tig .. 4 tig + 3, the D / 8 columns from gid D / 8 on.
 template <int D>
 struct Frag {
-    static constexpr int KW = D / 16;  // key words per token
-    static constexpr int VW = D / 32;  // value words per token
-    uint32_t k[2][KW];
-    uint32_t v[4][VW];
-
+    static constexpr int KW = D / 16;             // key words per token
+    static constexpr int VW = D / 32;             // value words per token
+    static constexpr int KB = D == 128 ? 16 : 8;  // bytes at a time: D = 96 has 24 and 12 a lane and token
+    static constexpr int VB = D == 128 ? 16 : 4;
+    static constexpr int KC = KW * 4 / KB, VC = VW * 4 / VB;  // of them per token
     __device__ __forceinline__ static int key_col(int w, int tig) {
-        return D == 128 ? (w >> 2) * 64 + tig * 16 + (w & 3) * 4 : (w >> 1) * 32 + tig * 8 + (w & 1) * 4;
+        return w * 4 / KB * (4 * KB) + tig * KB + w * 4 % KB;
     }
-    __device__ __forceinline__ void load_key(int i, const uint8_t* row, int tig) {
-        if constexpr (D == 128) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const uint4 x = ld_stream(row + c * 64 + tig * 16);
-                k[i][4 * c] = x.x;
-                k[i][4 * c + 1] = x.y;
-                k[i][4 * c + 2] = x.z;
-                k[i][4 * c + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                const uint2 x = ld_stream8(row + c * 32 + tig * 8);
-                k[i][2 * c] = x.x;
-                k[i][2 * c + 1] = x.y;
-            }
-        }
+    template <int N>
+    __device__ __forceinline__ static void get(uint32_t* w, const uint8_t* p) {
+        if constexpr (N == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (N == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+        else *w = *reinterpret_cast<const uint32_t*>(p);
     }
-    __device__ __forceinline__ void load_value(int i, const uint8_t* row, int gid) {
-        if constexpr (D == 128) {
-            const uint4 x = ld_stream(row + gid * 16);
-            v[i][0] = x.x;
-            v[i][1] = x.y;
-            v[i][2] = x.z;
-            v[i][3] = x.w;
-        } else {
+};
+
+// 16 rows of keys and of values, as they lie in the page. (Key reads meet
+// two to a bank; a swizzle would cost the bulk copies.)
+template <int D>
+struct PageStage : Frag<D> {
+    using F = Frag<D>;
+    uint8_t k[kTile][D], v[kTile][D];
+    __device__ __forceinline__ void get_key(int i, int lane, uint32_t* w) const {
+        const uint8_t* row = k[4 * (lane >> 3) + ((lane >> 2) & 1) + 2 * i];
 #pragma unroll
-            for (int c = 0; c < 3; ++c) v[i][c] = ld_stream4(row + gid * 12 + c * 4);
-        }
+        for (int c = 0; c < F::KC; ++c) F::template get<F::KB>(w + c * F::KB / 4, row + c * 4 * F::KB + (lane & 3) * F::KB);
     }
-    __device__ __forceinline__ void zero_key(int i) {
+    __device__ __forceinline__ void get_value(int i, int lane, uint32_t* w) const {
+        const uint8_t* row = v[4 * (lane & 3) + i] + (lane >> 2) * (D / 8);
 #pragma unroll
-        for (int w = 0; w < KW; ++w) k[i][w] = 0u;
+        for (int c = 0; c < F::VC; ++c) F::template get<F::VB>(w + c * F::VB / 4, row + c * F::VB);
     }
-    __device__ __forceinline__ void zero_value(int i) {
+};
+
+// Selected tokens: each lane's fragments side by side, a scale per token.
+template <int D>
+struct PickStage : Frag<D> {
+    using F = Frag<D>;
+    uint8_t k[2][F::KC][32][F::KB];
+    uint8_t v[4][F::VC][32][F::VB];
+    float ks[kTile], vs[kTile];
+    __device__ __forceinline__ void put_key(int i, const uint8_t* row, bool on, int lane) {
 #pragma unroll
-        for (int w = 0; w < VW; ++w) v[i][w] = 0u;
+        for (int c = 0; c < F::KC; ++c) copy_async<F::KB>(k[i][c][lane], row + c * 4 * F::KB + (lane & 3) * F::KB, on);
+    }
+    __device__ __forceinline__ void put_value(int i, const uint8_t* row, bool on, int lane) {
+#pragma unroll
+        for (int c = 0; c < F::VC; ++c) copy_async<F::VB>(v[i][c][lane], row + (lane >> 2) * (D / 8) + c * F::VB, on);
+    }
+    __device__ __forceinline__ void get_key(int i, int lane, uint32_t* w) const {
+#pragma unroll
+        for (int c = 0; c < F::KC; ++c) F::template get<F::KB>(w + c * F::KB / 4, k[i][c][lane]);
+    }
+    __device__ __forceinline__ void get_value(int i, int lane, uint32_t* w) const {
+#pragma unroll
+        for (int c = 0; c < F::VC; ++c) F::template get<F::VB>(w + c * F::VB / 4, v[i][c][lane]);
     }
 };
 
 // NT groups of up to four query heads of one KV head: their query fragments,
-// running softmax state and output accumulators. Lane (gid, tig) accumulates
-// head 4 t + tig, columns gid D / 8 ..; m is the same in the eight lanes of a
-// head, l is the lane's own tokens' share.
+// softmax state and output accumulators. Lane (gid, tig) accumulates head
+// 4 t + tig, columns gid D / 8 .., hi and lo parts apart, in units of 2^(m + E);
+// m and lift = 2^-E are the same in the eight lanes of a head, l is the lane's
+// own tokens' share.
 template <int D, int NT>
 struct Heads {
     static constexpr int KW = Frag<D>::KW, VW = Frag<D>::VW;
     uint32_t q[NT][KW][2];
-    float qs[NT], m[NT], l[NT], acc[NT][4 * VW];
+    float qs[NT], m[NT], lift[NT], l[NT], acc[NT][2 * VW][4];
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            m[t] = -INFINITY;
+            m[t] = kLeast;
+            lift[t] = 1.f;
             l[t] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4 * VW; ++i) acc[t][i] = 0.f;
+            for (int i = 0; i < 2 * VW; ++i) acc[t][i][0] = acc[t][i][1] = acc[t][i][2] = acc[t][i][3] = 0.f;
         }
     }
 
@@ -197,112 +234,137 @@ struct Heads {
         }
     }
 
-    // One tile: ok0, ok1 and the key scales k0, k1 are those of the lane's key
-    // tokens; the values of tokens left out are zero. One value scale for the
-    // tile (kOneScale: v0), or one per token (v0, v1).
-    template <bool kOneScale>
-    __device__ __forceinline__ void add(const Frag<D>& f, bool ok0, bool ok1, float k0, float k1, float v0,
-                                        float v1, int gid, int tig) {
-        float c[NT][4];
+    // One tile: ok0, ok1 and the scales k0 .. v1 are those of the lane's key
+    // tokens; of a partial tile only the first `valid` tokens' values count
+    // (behind them may lie NaN codes, which a zero weight would not stop).
+    template <class S>
+    __device__ __forceinline__ void add(const S& f, bool ok0, bool ok1, float k0, float k1, float v0, float v1,
+                                        bool partial, int valid, int lane) {
+        const int gid = lane >> 2, tig = lane & 3;
+        float c[NT][2][4];  // even and odd words: two chains of products
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[t][i] = 0.f;
+            for (int i = 0; i < 4; ++i) c[t][0][i] = c[t][1][i] = 0.f;
+        {
+            uint32_t ka[KW], kb[KW];
+            f.get_key(0, lane, ka);
+            f.get_key(1, lane, kb);
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            const uint32_t a0 = e4m3x2_to_f16x2(f.k[0][w] & 0xffffu), a1 = e4m3x2_to_f16x2(f.k[1][w] & 0xffffu);
-            const uint32_t a2 = e4m3x2_to_f16x2(f.k[0][w] >> 16), a3 = e4m3x2_to_f16x2(f.k[1][w] >> 16);
+            for (int w = 0; w < KW; ++w) {
+                const uint32_t a0 = e4m3x2_to_f16x2(ka[w] & 0xffffu), a1 = e4m3x2_to_f16x2(kb[w] & 0xffffu);
+                const uint32_t a2 = e4m3x2_to_f16x2(ka[w] >> 16), a3 = e4m3x2_to_f16x2(kb[w] >> 16);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(c[t], a0, a1, a2, a3, q[t][w][0], q[t][w][1]);
+                for (int t = 0; t < NT; ++t) mma_f16(c[t][w & 1], a0, a1, a2, a3, q[t][w][0], q[t][w][1]);
+            }
+        }
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.get_value(i, lane, v[i]);
+        if (partial) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * tig + i >= valid) {
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) v[i][w] = 0u;
+                }
         }
         uint32_t pf[NT][2];
-        float keep[NT], gain[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float x0 = ok0 ? (c[t][0] + c[t][1]) * qs[t] * k0 : -INFINITY;
-            const float x1 = ok1 ? (c[t][2] + c[t][3]) * qs[t] * k1 : -INFINITY;
-            float mt = fmaxf(x0, x1);
+            const float x0 = ok0 ? ((c[t][0][0] + c[t][1][0]) + (c[t][0][1] + c[t][1][1])) * qs[t] * k0 : -INFINITY;
+            const float x1 = ok1 ? ((c[t][0][2] + c[t][1][2]) + (c[t][0][3] + c[t][1][3])) * qs[t] * k1 : -INFINITY;
+            float u0 = exp2f(x0 - m[t]), u1 = exp2f(x1 - m[t]);
+            float w0 = u0 * lift[t] * v0, w1 = u1 * lift[t] * v1;
+            const float top = fmaxf(x0, x1);
+            if (__any_sync(0xffffffffu, top > m[t] + 8.f || fmaxf(w0, w1) > 32768.f)) {
+                float M = fmaxf(m[t], top);
 #pragma unroll
-            for (int off = 4; off <= 16; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-            const float M = fmaxf(m[t], mt);
-            keep[t] = m[t] == M ? 1.f : exp2f(m[t] - M);
-            // all of the tile's scores -inf: its weights are zero, not NaN (a
-            // NaN score makes p NaN, which l carries to the output)
-            const float base = mt == -INFINITY ? 0.f : mt;
-            float p0 = exp2f(x0 - base), p1 = exp2f(x1 - base);
-            gain[t] = mt == -INFINITY ? 0.f : exp2f(mt - M);
-            l[t] = l[t] * keep[t] + gain[t] * (p0 + p1);
-            m[t] = M;
-            float up = 32768.f;  // largest weight at 2^15
-            if constexpr (kOneScale) {
-                gain[t] *= v0 * (1.f / 32768.f);
-            } else {
-                p0 *= v0;
-                p1 *= v1;
-                float top = fmaxf(p0, p1);
+                for (int off = 4; off <= 16; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+                u0 = exp2f(x0 - M);
+                u1 = exp2f(x1 - M);
+                float y = fmaxf(u0 * v0, u1 * v1);
 #pragma unroll
-                for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                int e = 14 + 127 - (int)(__float_as_uint(top) >> 23);
-                e = e > 126 ? 126 : e;
-                up = __uint_as_float((uint32_t)(e + 127) << 23);
-                gain[t] *= __uint_as_float((uint32_t)(127 - e) << 23);
+                for (int off = 4; off <= 16; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+                // this tile's largest weighted value lies in 2^(M + E), 2^(M + E + 1), the others' in
+                // units of 2^(m + E before); 2^-E and its inverse stay far from fp32's ends
+                int E = max((int)(__float_as_uint(y) >> 23) - 127, -100);
+                const float keep = exp2f(m[t] - M);
+                if (keep > 0.f) E = max(E, 127 - (int)(__float_as_uint(lift[t]) >> 23) + (int)ceilf(m[t] - M));
+                const float up = __uint_as_float((uint32_t)(127 - E) << 23);
+                const float down = keep * (up / lift[t]);
+                l[t] *= keep;
+#pragma unroll
+                for (int i = 0; i < 2 * VW; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][i][e] *= down;
+                m[t] = M;
+                lift[t] = up;
+                w0 = u0 * up * v0;
+                w1 = u1 * up * v1;
             }
-            p0 *= up;
-            p1 *= up;
+            l[t] += u0 + u1;
             // column gid of the weights: head gid / 2, part gid % 2, of tokens 4 tig ..
             const int src = 8 * tig + (gid >> 1);
-            const float w0 = __shfl_sync(0xffffffffu, p0, src), w1 = __shfl_sync(0xffffffffu, p0, src + 4);
-            const float w2 = __shfl_sync(0xffffffffu, p1, src), w3 = __shfl_sync(0xffffffffu, p1, src + 4);
-            pf[t][0] = f16_part(w0, w1, gid & 1);
-            pf[t][1] = f16_part(w2, w3, gid & 1);
+            const float p0 = __shfl_sync(0xffffffffu, w0, src), p1 = __shfl_sync(0xffffffffu, w0, src + 4);
+            const float p2 = __shfl_sync(0xffffffffu, w1, src), p3 = __shfl_sync(0xffffffffu, w1, src + 4);
+            pf[t][0] = f16_part(p0, p1, gid & 1);
+            pf[t][1] = f16_part(p2, p3, gid & 1);
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 // bytes (A, B) of one column side by side, two columns a word
-                const uint32_t ab = __byte_perm(f.v[0][w], f.v[1][w], half ? 0x7362 : 0x5140);
-                const uint32_t cd = __byte_perm(f.v[2][w], f.v[3][w], half ? 0x7362 : 0x5140);
+                const uint32_t ab = __byte_perm(v[0][w], v[1][w], half ? 0x7362 : 0x5140);
+                const uint32_t cd = __byte_perm(v[2][w], v[3][w], half ? 0x7362 : 0x5140);
                 const uint32_t a0 = e4m3x2_to_f16x2(ab & 0xffffu), a1 = e4m3x2_to_f16x2(ab >> 16);
                 const uint32_t a2 = e4m3x2_to_f16x2(cd & 0xffffu), a3 = e4m3x2_to_f16x2(cd >> 16);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float o[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(o, a0, a1, a2, a3, pf[t][0], pf[t][1]);
-                    float* A = acc[t] + 4 * w + 2 * half;
-                    A[0] = fmaf(gain[t], o[0] + o[1], A[0] * keep[t]);
-                    A[1] = fmaf(gain[t], o[2] + o[3], A[1] * keep[t]);
-                }
+                for (int t = 0; t < NT; ++t) mma_f16(acc[t][2 * w + half], a0, a1, a2, a3, pf[t][0], pf[t][1]);
             }
         }
     }
 
-    // The state of rows row0 .. as output (slot < 0) or as the partial `slot`.
+    // column i of the lane's, in units of 2^(m + E)
+    __device__ __forceinline__ float col(int t, int i) const {
+        return acc[t][i >> 1][2 * (i & 1)] + acc[t][i >> 1][2 * (i & 1) + 1];
+    }
+
+    // The state of rows row0 .. row0 + G - 1 as output.
     template <class E>
-    __device__ __forceinline__ void store(const AttendQ8Args& a, int64_t row0, int G, int64_t slot, int gid,
-                                          int tig) {
-        float2* ml = static_cast<float2*>(a.ws);
-        float* pa = reinterpret_cast<float*>(ml + a.slots * G);
+    __device__ __forceinline__ void write(const AttendQ8Args& a, int64_t row0, int G, int gid, int tig) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int g = 4 * t + tig;
-            float L = l[t];
-#pragma unroll
-            for (int off = 4; off <= 16; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            const float L = sum(t);
             if (g >= G) continue;
-            if (slot < 0) {
-                typename E::T* o = static_cast<typename E::T*>(a.out) + (row0 + g) * D + gid * (D / 8);
-                const float r = L == 0.f ? 0.f : 1.f / L;
+            typename E::T* o = static_cast<typename E::T*>(a.out) + (row0 + g) * D + gid * (D / 8);
+            const float r = L == 0.f ? 0.f : 1.f / (L * lift[t]);
 #pragma unroll
-                for (int i = 0; i < 4 * VW; ++i) o[i] = E::from_float(acc[t][i] * r);
-            } else {
-                if (gid == 0) ml[slot * G + g] = make_float2(m[t], L);
-                float4* o = reinterpret_cast<float4*>(pa + (slot * G + g) * D + gid * (D / 8));
-#pragma unroll
-                for (int i = 0; i < VW; ++i)
-                    o[i] = make_float4(acc[t][4 * i], acc[t][4 * i + 1], acc[t][4 * i + 2], acc[t][4 * i + 3]);
-            }
+            for (int i = 0; i < 4 * VW; ++i) o[i] = E::from_float(col(t, i) * r);
         }
+    }
+    // The state as a partial: (max, sum) at ml[g], columns at pa[g D ..].
+    __device__ __forceinline__ void leave(float2* ml, float* pa, int G, int gid, int tig) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int g = 4 * t + tig;
+            const float L = sum(t);
+            if (g >= G) continue;
+            if (gid == 0) ml[g] = make_float2(m[t], L);
+            const float r = 1.f / lift[t];  // to units of 2^m
+            float4* o = reinterpret_cast<float4*>(pa + g * D + gid * (D / 8));
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+                o[i] = make_float4(col(t, 4 * i) * r, col(t, 4 * i + 1) * r, col(t, 4 * i + 2) * r, col(t, 4 * i + 3) * r);
+        }
+    }
+    __device__ __forceinline__ float sum(int t) const {
+        float L = l[t];
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        return L;
     }
 };
 
@@ -352,37 +414,116 @@ __device__ __forceinline__ int q8_find(const AttendQ8Args& a, int64_t w, int64_t
     return -1;
 }
 
-template <class E, int D, int NT>
-__global__ void __launch_bounds__(kQ8Threads, NT == 1 ? 4 : 3) k_dense_q8(const AttendQ8Args a) {
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const int64_t wi = (int64_t)blockIdx.x * (kQ8Threads / 32) + (threadIdx.x >> 5);
-    const int G = a.H_q / a.H_kv;
-    int64_t before, total;
-    q8_tiles(a, 0, &before, &total);
-    total *= a.H_kv;
-    const int64_t per = (total + a.warps - 1) / a.warps;
-    int64_t w = wi * per;
-    const int64_t w_end = min64(w + per, total);
-    if (w >= w_end) return;
-    int b = q8_find(a, w, &before);
-    if (b < 0) return;
-    int len = (int)q8_len(a, b);
-    int n = (len + kTile - 1) / kTile;  // tiles of a unit
-    int hk = (int)((w - before * a.H_kv) / n);
-    int t = (int)((w - before * a.H_kv) % n);
+// partial `slot` of G heads in the workspace
+__device__ __forceinline__ float2* slot_ml(const AttendQ8Args& a, int64_t slot, int G) {
+    return static_cast<float2*>(a.ws) + slot * G;
+}
+__device__ __forceinline__ float* slot_cols(const AttendQ8Args& a, int64_t slot, int G) {
+    return reinterpret_cast<float*>(static_cast<float2*>(a.ws) + a.slots * G) + slot * G * a.D;
+}
 
-    // the loads run one tile ahead of the arithmetic: lb, lhk, lt, ... are theirs
+// The cluster's partials of rows row0 .. row0 + G - 1 into the output: each
+// CTA merges its warps' in shared memory (which the tiles' rings leave free),
+// then takes a share of the outputs over the CTAs' merged ones.
+template <class E, int D, int NT>
+__device__ __forceinline__ void merge_cluster(const AttendQ8Args& a, Heads<D, NT>& h, uint8_t* smem, int64_t row0, int G) {
+    constexpr int W = kClThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2* ml = reinterpret_cast<float2*>(smem);       // [W][G], then the CTA's [G]
+    float* pa = reinterpret_cast<float*>(ml + 8 * (W + 1) );  // [W][G][D], then the CTA's [G][D]
+    __syncthreads();
+    h.leave(ml + warp * G, pa + warp * G * D, G, lane >> 2, lane & 3);
+    __syncthreads();
+    float2* cml = ml + W * G;
+    float* cpa = pa + W * G * D;
+    for (int i = threadIdx.x; i < G * D; i += kClThreads) {
+        const int g = i / D;
+        float M = -INFINITY, L = 0.f, A = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * G + g].x);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float2 x = ml[w * G + g];
+            const float s = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
+            L = fmaf(x.y, s, L);
+            A = fmaf(pa[w * G * D + i], s, A);
+        }
+        if (a.cluster == 1) {
+            static_cast<typename E::T*>(a.out)[row0 * D + i] = E::from_float(L == 0.f ? 0.f : A / L);
+        } else {
+            cpa[i] = A;
+            if (i % D == 0) cml[g] = make_float2(M, L);
+        }
+    }
+    if (a.cluster == 1) return;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int i = cl.block_rank() * kClThreads + threadIdx.x; i < G * D; i += a.cluster * kClThreads) {
+        const int g = i / D;
+        float M = -INFINITY, L = 0.f, A = 0.f;
+        for (int r = 0; r < a.cluster; ++r) M = fmaxf(M, cl.map_shared_rank(cml, r)[g].x);
+        for (int r = 0; r < a.cluster; ++r) {
+            const float2 x = cl.map_shared_rank(cml, r)[g];
+            const float s = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
+            L = fmaf(x.y, s, L);
+            A = fmaf(cl.map_shared_rank(cpa, r)[i], s, A);
+        }
+        static_cast<typename E::T*>(a.out)[row0 * D + i] = E::from_float(L == 0.f ? 0.f : A / L);
+    }
+    cl.sync();  // the others may still read this CTA's
+}
+
+// kCl: a cluster per (sequence, KV head), a run of its tiles per warp.
+template <class E, int D, int NT, bool kCl>
+__global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl ? 2 : 4) : (kCl ? 1 : 3))
+    k_dense_q8(const AttendQ8Args a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+    PageStage<D>* ring = reinterpret_cast<PageStage<D>*>(smem) + warp * kStages;
+    __shared__ __align__(8) uint64_t bars[(kCl ? kClThreads : kQ8Threads) / 32][kStages];
+    uint64_t* bar = bars[warp];
+    if (lane < kStages) mbar_init(bar + lane, 1);
+    fence_mbar_init();
+    __syncwarp();
+    const int64_t wi = (int64_t)blockIdx.x * (kQ8Threads / 32) + warp;
+    const int G = a.H_q / a.H_kv;
+    int b, hk, len, n, t;  // n: tiles of the unit, t: the next one
+    int64_t w, w_end;
+    if constexpr (kCl) {
+        const int unit = blockIdx.x / a.cluster, cw = blockIdx.x % a.cluster * (kClThreads / 32) + warp;
+        b = unit / a.H_kv;
+        hk = unit % a.H_kv;
+        len = (int)q8_len(a, b);
+        n = (len + kTile - 1) / kTile;
+        const int cws = a.cluster * (kClThreads / 32), per = (n + cws - 1) / cws;
+        w = t = cw * per;
+        w_end = min(t + per, n);
+    } else {
+        int64_t before, total;
+        q8_tiles(a, 0, &before, &total);
+        total *= a.H_kv;
+        const int64_t per = (total + a.warps - 1) / a.warps;
+        w = wi * per;
+        w_end = min64(w + per, total);
+        if (w >= w_end) return;
+        b = q8_find(a, w, &before);
+        if (b < 0) return;
+        len = (int)q8_len(a, b);
+        n = (len + kTile - 1) / kTile;
+        hk = (int)((w - before * a.H_kv) / n);
+        t = (int)((w - before * a.H_kv) % n);
+    }
+
+    // the copies run kStages - 1 tiles ahead of the arithmetic: lb, lhk, lt, ... are theirs
     int lb = b, lhk = hk, lt = t, llen = len, ln = n;
     int lp = -1, lpage = -1, loff = 0;  // page index, page, first token in it
-    const uint8_t *K = nullptr, *V = nullptr;
-    struct Next {
-        Frag<D> f;
-        float ks, vs;
-        int valid;
-    } nx, cu;
     const int tk = 4 * (gid >> 1) + (gid & 1);
-    auto load = [&](Next& x) {
+    // issues the next tile's copies; how many of its tokens count, its scales' index
+    struct Tile {
+        int valid, blk;
+    };
+    auto load = [&](int at) -> Tile {
         const int j = lt * kTile;
         if (lp < 0) {
             lp = j / a.page_size;
@@ -393,27 +534,25 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 ? 4 : 3) k_dense_q8(const 
             loff = 0;
             lpage = __ldg(a.block_table + (int64_t)lb * a.max_pages + lp);
         }
+        Tile x{0, 0};
         if (lpage >= 0 && lpage < a.n_pages) {
-            const int64_t row = ((int64_t)lpage * a.H_kv + lhk) * a.page_size + loff;
-            K = a.K_pages + row * D;
-            V = a.V_pages + row * D;
-            x.valid = llen - j;
-            x.f.load_key(0, K + tk * D, tig);
-            x.f.load_key(1, K + (tk + 2) * D, tig);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.f.load_value(i, V + (4 * tig + i) * D, gid);
-            const int64_t blk = row >> a.block_log2;
-            x.ks = __ldg(a.k_scales + blk);
-            x.vs = __ldg(a.v_scales + blk);
-        } else {
-            x.valid = 0;
-            if (lane == 0) atomicExch(a.err, kDevErrBadPage);
+            x.valid = min(llen - j, kTile);
+            const int row = (lpage * a.H_kv + lhk) * a.page_size + loff;
+            x.blk = row >> a.block_log2;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar + at, 2 * kTile * D);
+                bulk_load(ring[at].k, a.K_pages + (int64_t)row * D, kTile * D, bar + at);
+                bulk_load(ring[at].v, a.V_pages + (int64_t)row * D, kTile * D, bar + at);
+            }
+        } else if (lane == 0) {
+            mbar_arrive(bar + at);  // nothing to wait for
+            atomicExch(a.err, kDevErrBadPage);
         }
         loff += kTile;
         if (++lt == ln) {  // the next unit with tokens
             lt = 0;
             lp = -1;
-            if (++lhk == a.H_kv) {
+            if (!kCl && ++lhk == a.H_kv) {
                 lhk = 0;
                 do {
                     if (++lb >= a.B) break;
@@ -422,30 +561,40 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 ? 4 : 3) k_dense_q8(const 
                 ln = (llen + kTile - 1) / kTile;
             }
         }
+        return x;
     };
 
+    Tile tile[kStages] = {};  // the one at hand and the ones behind it
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        if (w + i < w_end) tile[i] = load(i);
+    float ks = __ldg(a.k_scales + tile[0].blk), vs = __ldg(a.v_scales + tile[0].blk);
     Heads<D, NT> h;
     h.reset();
     h.load(a, (int64_t)b * a.H_q + (int64_t)hk * G, G, gid, tig);
     bool whole = t == 0;
-    load(cu);
-    while (true) {
-        const bool more = w + 1 < w_end;
-        if (more) load(nx);
-        if (cu.valid > 0) {
-            if (cu.valid < kTile) {
+    uint32_t phase = 0;
+    bool alive = true;
+    for (int at = 0; w < w_end; phase ^= at + 1 == kStages, at = at + 1 == kStages ? 0 : at + 1) {
+        __syncwarp();  // every lane is done with the stage before this one
+        if (w + kStages - 1 < w_end) tile[kStages - 1] = load(at == 0 ? kStages - 1 : at - 1);
+        const float ks1 = __ldg(a.k_scales + tile[1].blk), vs1 = __ldg(a.v_scales + tile[1].blk);
+        alive = mbar_wait(bar + at, phase, a.err);
+        if (!__all_sync(0xffffffffu, alive)) break;  // flagged; nothing waits for the rest
+        const int valid = tile[0].valid;
+        if (valid > 0)
+            h.add(ring[at], tk < valid, tk + 2 < valid, ks, ks, vs, vs, valid < kTile, valid, lane);
+        ks = ks1;
+        vs = vs1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * tig + i >= cu.valid) cu.f.zero_value(i);
-            }
-            h.template add<true>(cu.f, tk < cu.valid, tk + 2 < cu.valid, cu.ks, cu.ks, cu.vs, cu.vs, gid, tig);
-        }
+        for (int i = 0; i + 1 < kStages; ++i) tile[i] = tile[i + 1];
         ++t;
         ++w;
-        if (t == n || !more) {
+        if (!kCl && (t == n || w == w_end)) {
             const int64_t unit = (int64_t)b * a.H_kv + hk;
-            h.template store<E>(a, unit * G, G, whole && t == n ? -1 : unit + wi, gid, tig);
-            if (!more) return;
+            if (whole && t == n) h.template write<E>(a, unit * G, G, gid, tig);
+            else h.leave(slot_ml(a, unit + wi, G), slot_cols(a, unit + wi, G), G, gid, tig);
+            if (w == w_end) return;
             t = 0;
             whole = true;
             if (++hk == a.H_kv) {
@@ -459,31 +608,46 @@ __global__ void __launch_bounds__(kQ8Threads, NT == 1 ? 4 : 3) k_dense_q8(const 
             h.reset();
             h.load(a, (int64_t)b * a.H_q + (int64_t)hk * G, G, gid, tig);
         }
-        cu = nx;
     }
+    if constexpr (kCl) merge_cluster<E>(a, h, smem, ((int64_t)b * a.H_kv + hk) * G, G);
 }
 
 // Selected tokens: a tile is 16 consecutive entries of a row's list; lane l
-// looks up entry l % 16 and hands its row number to the lanes that load it.
-template <class E, int D>
-__global__ void __launch_bounds__(kQ8Threads, 4) k_sparse_q8(const AttendQ8Args a) {
+// looks up entry l % 16 and hands its row number to the lanes that copy it.
+// kCl: a cluster per (sequence, query head), a run of its tiles per warp.
+template <class E, int D, bool kCl>
+__global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, kCl ? 2 : 4) k_sparse_q8(const AttendQ8Args a) {
+    extern __shared__ __align__(16) uint8_t smem[];
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const int64_t wi = (int64_t)blockIdx.x * (kQ8Threads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+    PickStage<D>* ring = reinterpret_cast<PickStage<D>*>(smem) + warp * kStages;
+    const int64_t wi = (int64_t)blockIdx.x * (kQ8Threads / 32) + warp;
     const int G = a.H_q / a.H_kv;
-    const int64_t n = (a.k + kTile - 1) / kTile, total = n * a.B * a.H_q;
-    const int64_t per = (total + a.warps - 1) / a.warps;
-    int64_t w = wi * per;
-    const int64_t w_end = min64(w + per, total);
-    if (w >= w_end) return;
-    int64_t r = w / n, t = w % n;
+    const int64_t n = (a.k + kTile - 1) / kTile;
+    int64_t w, w_end, r, t;
+    if constexpr (kCl) {
+        r = blockIdx.x / a.cluster;
+        const int cws = a.cluster * (kClThreads / 32);
+        const int64_t per = (n + cws - 1) / cws;
+        w = t = (blockIdx.x % a.cluster * (kClThreads / 32) + warp) * per;
+        w_end = min64(t + per, n);
+    } else {
+        const int64_t total = n * a.B * a.H_q, per = (total + a.warps - 1) / a.warps;
+        w = wi * per;
+        w_end = min64(w + per, total);
+        if (w >= w_end) return;
+        r = w / n;
+        t = w % n;
+    }
     const int tk = 4 * (gid >> 1) + (gid & 1);
 
-    // entries run two tiles ahead of the arithmetic, rows one
-    int64_t ir = r, it = t;
+    // entries run kStages tiles ahead of the arithmetic, copies one less
+    int64_t ir = r, it = t, iw = w;
     auto entry = [&]() -> int {
+        if (iw >= w_end) return -1;
         const int64_t e = it * kTile + (lane & 15);
         const int j = e < a.k ? __ldg(a.idx + ir * a.k + e) : -1;
+        ++iw;
         if (++it == n) {
             it = 0;
             ++ir;
@@ -492,38 +656,32 @@ __global__ void __launch_bounds__(kQ8Threads, 4) k_sparse_q8(const AttendQ8Args 
     };
     int64_t lr = r, lt = t;
     int lb = (int)(r / a.H_q), lhk = (int)(r % a.H_q) / G, llen = (int)q8_len(a, lb);
-    struct Next {
-        Frag<D> f;
-        float ks, vs;  // of entry lane % 16
-        uint32_t ok;   // bit per entry
-    } nx, cu;
-    auto load = [&](Next& x, int j) {
+    // issues the copies of the tile with entries j; a bit for each that counts
+    auto load = [&](PickStage<D>& x, int j) -> uint32_t {
         uint32_t row = kNoRow;
-        x.ks = x.vs = 0.f;
         if (j >= 0 && j < llen) {
             const uint32_t lp = a.page_log2 >= 0 ? (uint32_t)j >> a.page_log2 : (uint32_t)j / (uint32_t)a.page_size;
             const int page = __ldg(a.block_table + (int64_t)lb * a.max_pages + lp);
-            if (page >= 0 && page < a.n_pages) {
+            if (page >= 0 && page < a.n_pages)
                 row = ((uint32_t)page * a.H_kv + lhk) * a.page_size + ((uint32_t)j - lp * a.page_size);
-                x.ks = __ldg(a.k_scales + (row >> a.block_log2));
-                x.vs = __ldg(a.v_scales + (row >> a.block_log2));
-            } else {
+            else
                 atomicExch(a.err, kDevErrBadPage);
-            }
         }
-        x.ok = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
-        if (x.ok != 0) {
+        const uint32_t ok = __ballot_sync(0xffffffffu, row != kNoRow) & 0xffffu;
+        if (ok != 0) {
+            const bool on = row != kNoRow;
+            const uint32_t blk = on ? row >> a.block_log2 : 0u;
+            if (lane < kTile) copy_async<4>(x.ks + lane, a.k_scales + blk, on);
+            else copy_async<4>(x.vs + (lane - kTile), a.v_scales + blk, on);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t rr = __shfl_sync(0xffffffffu, row, tk + 2 * i);
-                if (rr != kNoRow) x.f.load_key(i, a.K_pages + (int64_t)rr * D, tig);
-                else x.f.zero_key(i);
+                x.put_key(i, a.K_pages + (rr != kNoRow ? (int64_t)rr * D : 0), rr != kNoRow, lane);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t rr = __shfl_sync(0xffffffffu, row, 4 * tig + i);
-                if (rr != kNoRow) x.f.load_value(i, a.V_pages + (int64_t)rr * D, gid);
-                else x.f.zero_value(i);
+                x.put_value(i, a.V_pages + (rr != kNoRow ? (int64_t)rr * D : 0), rr != kNoRow, lane);
             }
         }
         if (++lt == n) {
@@ -534,40 +692,50 @@ __global__ void __launch_bounds__(kQ8Threads, 4) k_sparse_q8(const AttendQ8Args 
                 llen = (int)q8_len(a, lb);
             }
         }
+        return ok;
     };
 
+    uint32_t ok[kStages] = {};  // of the tile at hand and the ones behind it
+    int j = entry();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        const int j0 = j;
+        j = entry();
+        if (w + i < w_end) ok[i] = load(ring[i], j0);
+        copy_commit();
+    }
     Heads<D, 1> h;
     h.reset();
-    const int j0 = entry();
-    int j1 = w + 1 < w_end ? entry() : -1;
     h.load(a, r, 1, gid, tig);
     bool whole = t == 0;
-    load(cu, j0);
-    while (true) {
-        const bool more = w + 1 < w_end;
-        if (more) {
-            const int j = j1;
-            if (w + 2 < w_end) j1 = entry();
-            load(nx, j);
+    for (int at = 0; w < w_end; at = at + 1 == kStages ? 0 : at + 1) {
+        const int j0 = j;
+        j = entry();
+        copy_wait<kStages - 2>();
+        __syncwarp();  // every lane's copies have landed, and every lane is done with the stage before
+        if (w + kStages - 1 < w_end) ok[kStages - 1] = load(ring[at == 0 ? kStages - 1 : at - 1], j0);
+        copy_commit();
+        if (ok[0] != 0) {
+            const PickStage<D>& x = ring[at];
+            h.add(x, (ok[0] >> tk) & 1u, (ok[0] >> (tk + 2)) & 1u, x.ks[tk], x.ks[tk + 2], x.vs[tk], x.vs[tk + 2],
+                  false, kTile, lane);
         }
-        if (cu.ok != 0) {
-            const float k0 = __shfl_sync(0xffffffffu, cu.ks, tk), k1 = __shfl_sync(0xffffffffu, cu.ks, tk + 2);
-            const float v0 = __shfl_sync(0xffffffffu, cu.vs, tk), v1 = __shfl_sync(0xffffffffu, cu.vs, tk + 2);
-            h.template add<false>(cu.f, (cu.ok >> tk) & 1u, (cu.ok >> (tk + 2)) & 1u, k0, k1, v0, v1, gid, tig);
-        }
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; ++i) ok[i] = ok[i + 1];
         ++t;
         ++w;
-        if (t == n || !more) {
-            h.template store<E>(a, r, 1, whole && t == n ? -1 : r + wi, gid, tig);
-            if (!more) return;
+        if (!kCl && (t == n || w == w_end)) {
+            if (whole && t == n) h.template write<E>(a, r, 1, gid, tig);
+            else h.leave(slot_ml(a, r + wi, 1), slot_cols(a, r + wi, 1), 1, gid, tig);
+            if (w == w_end) return;
             t = 0;
             whole = true;
             ++r;
             h.reset();
             h.load(a, r, 1, gid, tig);
         }
-        cu = nx;
     }
+    if constexpr (kCl) merge_cluster<E>(a, h, smem, r, 1);
 }
 
 // Merges the partials of one (sequence, query head) row: the warps take
@@ -606,9 +774,8 @@ __global__ void __launch_bounds__(128) k_q8_combine(const AttendQ8Args a) {
     const int64_t c0 = first / per;
     const int np = (int)(last / per - c0 + 1);
     if (np == 1 && first % per + (last - first) < per) return;
-    const float2* ml = static_cast<const float2*>(a.ws) + (unit + c0) * Gc + g;
-    const float* pa = reinterpret_cast<const float*>(static_cast<const float2*>(a.ws) + a.slots * Gc) +
-                      ((unit + c0) * Gc + g) * D;
+    const float2* ml = slot_ml(a, unit + c0, Gc) + g;
+    const float* pa = slot_cols(a, unit + c0, Gc) + g * D;
     float M = -INFINITY;
     for (int p = threadIdx.x; p < np; p += 128) M = fmaxf(M, ml[(int64_t)p * Gc].x);
 #pragma unroll
@@ -666,25 +833,64 @@ size_t sparse_q8_ws_bytes(int B, int H_q, int64_t k, int D) {
     return q8_ws_bytes(rows, rows * ((k + kTile - 1) / kTile), 1, D);
 }
 
+// CTAs of a cluster: as many as keep all clusters resident together, while
+// every warp has a tile. 0: too many tiles a warp, the two-kernel form.
+static int cluster_size(int64_t units, int64_t tiles, int64_t resident) {
+    constexpr int W = kClThreads / 32;
+    int c = 8;
+    while (c > 1 && (units * c > resident || (c / 2) * W >= tiles)) c >>= 1;
+    return (tiles + c * W - 1) / (c * W) <= kClusterTiles ? c : 0;
+}
+
 template <class E, int D>
 static cudaError_t attend_impl(AttendQ8Args& a, cudaStream_t s) {
     const int G = a.H_q / a.H_kv;
-    auto kern = a.idx != nullptr ? k_sparse_q8<E, D> : G <= 4 ? k_dense_q8<E, D, 1> : k_dense_q8<E, D, 2>;
+    const bool sparse = a.idx != nullptr;
     DevInfo di;
     cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
-    // no shared memory: the table, scale and index loads want the L1
-    e = prefer_carveout((const void*)kern, cudaSharedmemCarveoutMaxL1);
+    const int64_t units = sparse ? (int64_t)a.B * a.H_q : (int64_t)a.B * a.H_kv;
+    const int64_t items = sparse ? a.k : (int64_t)a.page_size * a.max_pages;
+    const int64_t tiles = (items + kTile - 1) / kTile;
+    auto size = [=](const void* f, int threads, size_t* smem) {
+        *smem = (size_t)threads / 32 * kStages * (sparse ? sizeof(PickStage<D>) : sizeof(PageStage<D>));
+        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*smem);
+    };
+    size_t smem;
+    auto ck = sparse   ? k_sparse_q8<E, D, true>
+              : G <= 4 ? k_dense_q8<E, D, 1, true>
+                       : k_dense_q8<E, D, 2, true>;
+    e = size((const void*)ck, kClThreads, &smem);
     if (e != cudaSuccess) return e;
-    const int64_t units = a.idx != nullptr ? (int64_t)a.B * a.H_q : (int64_t)a.B * a.H_kv;
-    const int64_t items = a.idx != nullptr ? a.k : (int64_t)a.page_size * a.max_pages;
-    const int64_t tiles = units * ((items + kTile - 1) / kTile);
+    a.cluster = cluster_size(units, tiles, (int64_t)di.sm_count * occupancy((const void*)ck, kClThreads, smem));
+    if (a.cluster > 0 && units * a.cluster <= 0x7fffffff) {
+        e = prefer_carveout((const void*)ck, cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(units * a.cluster));
+        cfg.blockDim = dim3(kClThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = a.cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, ck, a);
+    }
+    auto kern = sparse   ? k_sparse_q8<E, D, false>
+                : G <= 4 ? k_dense_q8<E, D, 1, false>
+                         : k_dense_q8<E, D, 2, false>;
+    e = size((const void*)kern, kQ8Threads, &smem);
+    if (e != cudaSuccess) return e;
     const int wpc = kQ8Threads / 32;
-    int64_t warps = (int64_t)di.sm_count * occupancy((const void*)kern, kQ8Threads, 0) * wpc;
-    warps = min64(min64(warps, kQ8MaxWarps), tiles);
+    int64_t warps = (int64_t)di.sm_count * occupancy((const void*)kern, kQ8Threads, smem) * wpc;
+    warps = min64(min64(warps, kQ8MaxWarps), units * tiles);
     a.warps = (int)warps;
-    a.slots = q8_slots(units, tiles);
-    e = launch_kernel(kern, dim3((unsigned)((warps + wpc - 1) / wpc)), dim3(kQ8Threads), 0, s, false, a);
+    a.slots = q8_slots(units, units * tiles);
+    e = launch_kernel(kern, dim3((unsigned)((warps + wpc - 1) / wpc)), dim3(kQ8Threads), smem, s, false, a);
     if (e != cudaSuccess) return e;
     return launch_kernel(k_q8_combine<E, D>, dim3((unsigned)((int64_t)a.B * a.H_q)), dim3(128), 0, s, true, a);
 }

@@ -225,7 +225,7 @@ struct AttendQ8Args {
     void* ws = nullptr;
     // set by the launcher
     int page_log2 = 0;  // -1: not a power of two
-    int block_log2 = 0, warps = 0;
+    int block_log2 = 0, warps = 0, cluster = 0;
     int64_t slots = 0;
     int* err = nullptr;
 };
