@@ -38,14 +38,20 @@
 // fetching and reading back its own fragments.
 //
 // The tiles of all (sequence, KV head) units - of all (sequence, query head)
-// rows, when tokens are selected - are laid end to end and dealt to the
-// resident warps in equal runs. A warp that owns a whole unit writes its
-// output, others leave partials (fp32 max, sum, D columns per head) that
-// k_q8_combine merges in a fixed order. Where that would leave a warp only a
+// rows, when tokens are selected - are laid end to end and dealt to warps in
+// runs: four fifths of the line to the warps that are resident together, the
+// last fifth in runs a quarter as long to as many warps behind them, which
+// the SMs that are done first take up (SMs differ by 15 % in what the memory
+// gives them; equal runs left the others idle for a fifth of the time).
+// Which warp reduces which tiles is fixed all the same. A warp that owns a
+// whole unit writes its output, others leave partials (fp32 max, sum, D
+// columns per head) that k_q8_combine merges in a fixed order. Where that would leave a warp only a
 // few tiles, latency counts, and one kernel does it all: a cluster of CTAs
 // takes a unit, its warps a run of tiles each, and the partials meet in
 // shared memory, the CTAs' through distributed shared memory.
 #include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "launch.h"
@@ -59,8 +65,8 @@ namespace cg = cooperative_groups;
 constexpr int kQ8Threads = 128;
 constexpr int kClThreads = 256;  // of the cluster kernels
 constexpr int kStages = 3;
-constexpr int kClusterTiles = 8;  // the most tiles a warp of theirs takes
-constexpr int kQ8MaxWarps = 148 * 16;  // workspace is laid out for at most this many
+constexpr int kClusterTiles = 4;  // the most tiles a warp of theirs takes
+constexpr int kQ8MaxWarps = 2 * 148 * 16;  // workspace is laid out for at most this many
 constexpr int kTile = 16;
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLeast = -3.402823466e38f;  // below every score
@@ -85,6 +91,22 @@ __device__ __forceinline__ uint32_t f16_part(float x, float y, bool rest) {
     return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// 2^x to 2 ulp; results below 2^-126 are zero
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// box {D, 16} of a [rows, D] byte matrix, from its row `row` on
+__device__ __forceinline__ void tile_load(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(0), "r"(row), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // N bytes (4, 8 or 16) to shared memory, zeros when !on
 template <int N>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
@@ -102,9 +124,12 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // A tile in shared memory. Lane (gid = lane / 4, tig = lane % 4) reads
-//   keys:   tokens tk = 4 (gid / 2) + gid % 2 and tk + 2, the columns
+//   keys:   tokens key_token(gid) and the one eight behind it, the columns
 //           key_col(w, tig) .. + 3 as word w;
-//   values: tokens 4 tig .. 4 tig + 3, the D / 8 columns from gid D / 8 on.
+//   values: tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9, the D / 8 columns
+//           from gid D / 8 on.
+// Eight lanes that read together so touch rows four or two apart, which the
+// 128-byte swizzle of PageStage spreads over all banks.
 template <int D>
 struct Frag {
     static constexpr int KW = D / 16;             // key words per token
@@ -115,6 +140,8 @@ struct Frag {
     __device__ __forceinline__ static int key_col(int w, int tig) {
         return w * 4 / KB * (4 * KB) + tig * KB + w * 4 % KB;
     }
+    __device__ __forceinline__ static int key_token(int gid) { return (gid >> 1) + 4 * (gid & 1); }
+    __device__ __forceinline__ static int value_token(int i, int tig) { return 2 * tig + (i & 1) + 8 * (i >> 1); }
     template <int N>
     __device__ __forceinline__ static void get(uint32_t* w, const uint8_t* p) {
         if constexpr (N == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
@@ -123,21 +150,28 @@ struct Frag {
     }
 };
 
-// 16 rows of keys and of values, as they lie in the page. (Key reads meet
-// two to a bank; a swizzle would cost the bulk copies.)
+// 16 rows of keys and of values as they lie in the page; D = 128: the 16-byte
+// chunk c of row r at c ^ (r % 8), as the tensor map's 128-byte swizzle puts it.
 template <int D>
 struct PageStage : Frag<D> {
     using F = Frag<D>;
     uint8_t k[kTile][D], v[kTile][D];
+    __device__ __forceinline__ static int chunk(int c, int row) { return (D == 128 ? c ^ (row & 7) : c) * 16; }
     __device__ __forceinline__ void get_key(int i, int lane, uint32_t* w) const {
-        const uint8_t* row = k[4 * (lane >> 3) + ((lane >> 2) & 1) + 2 * i];
+        const int r = F::key_token(lane >> 2) + 8 * i;
 #pragma unroll
-        for (int c = 0; c < F::KC; ++c) F::template get<F::KB>(w + c * F::KB / 4, row + c * 4 * F::KB + (lane & 3) * F::KB);
+        for (int c = 0; c < F::KC; ++c) {
+            const int at = D == 128 ? chunk(4 * c + (lane & 3), r) : c * 4 * F::KB + (lane & 3) * F::KB;
+            F::template get<F::KB>(w + c * F::KB / 4, k[r] + at);
+        }
     }
     __device__ __forceinline__ void get_value(int i, int lane, uint32_t* w) const {
-        const uint8_t* row = v[4 * (lane & 3) + i] + (lane >> 2) * (D / 8);
+        const int r = F::value_token(i, lane & 3);
 #pragma unroll
-        for (int c = 0; c < F::VC; ++c) F::template get<F::VB>(w + c * F::VB / 4, row + c * F::VB);
+        for (int c = 0; c < F::VC; ++c) {
+            const int at = D == 128 ? chunk(lane >> 2, r) : (lane >> 2) * (D / 8) + c * F::VB;
+            F::template get<F::VB>(w + c * F::VB / 4, v[r] + at);
+        }
     }
 };
 
@@ -264,7 +298,7 @@ struct Heads {
         if (partial) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (4 * tig + i >= valid) {
+                if (Frag<D>::value_token(i, tig) >= valid) {
 #pragma unroll
                     for (int w = 0; w < VW; ++w) v[i][w] = 0u;
                 }
@@ -274,15 +308,15 @@ struct Heads {
         for (int t = 0; t < NT; ++t) {
             const float x0 = ok0 ? ((c[t][0][0] + c[t][1][0]) + (c[t][0][1] + c[t][1][1])) * qs[t] * k0 : -INFINITY;
             const float x1 = ok1 ? ((c[t][0][2] + c[t][1][2]) + (c[t][0][3] + c[t][1][3])) * qs[t] * k1 : -INFINITY;
-            float u0 = exp2f(x0 - m[t]), u1 = exp2f(x1 - m[t]);
+            float u0 = exp2_fast(x0 - m[t]), u1 = exp2_fast(x1 - m[t]);
             float w0 = u0 * lift[t] * v0, w1 = u1 * lift[t] * v1;
             const float top = fmaxf(x0, x1);
             if (__any_sync(0xffffffffu, top > m[t] + 8.f || fmaxf(w0, w1) > 32768.f)) {
                 float M = fmaxf(m[t], top);
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-                u0 = exp2f(x0 - M);
-                u1 = exp2f(x1 - M);
+                u0 = exp2_fast(x0 - M);
+                u1 = exp2_fast(x1 - M);
                 float y = fmaxf(u0 * v0, u1 * v1);
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
@@ -304,10 +338,11 @@ struct Heads {
                 w1 = u1 * up * v1;
             }
             l[t] += u0 + u1;
-            // column gid of the weights: head gid / 2, part gid % 2, of tokens 4 tig ..
-            const int src = 8 * tig + (gid >> 1);
-            const float p0 = __shfl_sync(0xffffffffu, w0, src), p1 = __shfl_sync(0xffffffffu, w0, src + 4);
-            const float p2 = __shfl_sync(0xffffffffu, w1, src), p3 = __shfl_sync(0xffffffffu, w1, src + 4);
+            // column gid of the weights (head gid / 2, part gid % 2) of this lane's value tokens, from
+            // the lanes that hold them as key tokens
+            const int src = 16 * (tig & 1) + 4 * (tig >> 1) + (gid >> 1);
+            const float p0 = __shfl_sync(0xffffffffu, w0, src), p1 = __shfl_sync(0xffffffffu, w0, src + 8);
+            const float p2 = __shfl_sync(0xffffffffu, w1, src), p3 = __shfl_sync(0xffffffffu, w1, src + 8);
             pf[t][0] = f16_part(p0, p1, gid & 1);
             pf[t][1] = f16_part(p2, p3, gid & 1);
         }
@@ -389,6 +424,33 @@ __device__ __forceinline__ void q8_tiles(const AttendQ8Args& a, int b, int64_t* 
     *before = x;
     *total = y;
 }
+
+// a / b, b > 0: most lines of tiles are short enough for the 32-bit division
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The line of `total` tiles in runs: a.warps / 2 of `per`, then a.warps / 2 of `tail`.
+struct Runs {
+    int64_t per, tail, split, total;  // split: where the short runs begin
+    int first;                        // warps with long runs
+    __device__ __forceinline__ Runs(const AttendQ8Args& a, int64_t n) : total(n), first(a.warps >> 1) {
+        per = quot(n * 4, 5 * (int64_t)first);
+        per = per < 1 ? 1 : per;
+        split = min64(per * first, n);
+        tail = quot(n - split + first - 1, first);
+        tail = tail < 1 ? 1 : tail;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t w) const {
+        return min64(w < first ? w * per : split + (w - first) * tail, total);
+    }
+    __device__ __forceinline__ int64_t end(int64_t w) const {
+        return w < first ? min64(w * per + per, split) : min64(split + (w - first + 1) * tail, total);
+    }
+    __device__ __forceinline__ int64_t owner(int64_t tile) const {
+        return tile < split ? quot(tile, per) : first + quot(tile - split, tail);
+    }
+};
 
 // the sequence of tile w (counting H_kv runs of tiles per sequence)
 __device__ __forceinline__ int q8_find(const AttendQ8Args& a, int64_t w, int64_t* before) {
@@ -476,8 +538,9 @@ __device__ __forceinline__ void merge_cluster(const AttendQ8Args& a, Heads<D, NT
 // kCl: a cluster per (sequence, KV head), a run of its tiles per warp.
 template <class E, int D, int NT, bool kCl>
 __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl ? 2 : 4) : (kCl ? 1 : 3))
-    k_dense_q8(const AttendQ8Args a) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    k_dense_q8(const AttendQ8Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;  // the swizzle goes by address
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
     PageStage<D>* ring = reinterpret_cast<PageStage<D>*>(smem) + warp * kStages;
@@ -502,23 +565,23 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
     } else {
         int64_t before, total;
         q8_tiles(a, 0, &before, &total);
-        total *= a.H_kv;
-        const int64_t per = (total + a.warps - 1) / a.warps;
-        w = wi * per;
-        w_end = min64(w + per, total);
+        const Runs runs(a, total * a.H_kv);  // (q8_find's lengths come from the L1)
+        w = runs.begin(wi);
+        w_end = runs.end(wi);
         if (w >= w_end) return;
         b = q8_find(a, w, &before);
         if (b < 0) return;
         len = (int)q8_len(a, b);
         n = (len + kTile - 1) / kTile;
-        hk = (int)((w - before * a.H_kv) / n);
-        t = (int)((w - before * a.H_kv) % n);
+        hk = (int)quot(w - before * a.H_kv, n);
+        t = (int)(w - before * a.H_kv - (int64_t)hk * n);
     }
 
     // the copies run kStages - 1 tiles ahead of the arithmetic: lb, lhk, lt, ... are theirs
     int lb = b, lhk = hk, lt = t, llen = len, ln = n;
-    int lp = -1, lpage = -1, loff = 0;  // page index, page, first token in it
-    const int tk = 4 * (gid >> 1) + (gid & 1);
+    int lp = -1, lpage = -1, lnext = -1, loff = 0;  // page index, page and the one behind, first token in it
+    const int tk = Frag<D>::key_token(gid);
+    auto page = [&](int i) { return __ldg(a.block_table + (int64_t)lb * a.max_pages + min(i, a.max_pages - 1)); };
     // issues the next tile's copies; how many of its tokens count, its scales' index
     struct Tile {
         int valid, blk;
@@ -528,11 +591,13 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
         if (lp < 0) {
             lp = j / a.page_size;
             loff = j - lp * a.page_size;
-            lpage = __ldg(a.block_table + (int64_t)lb * a.max_pages + lp);
+            lpage = page(lp);
+            lnext = page(lp + 1);
         } else if (loff == a.page_size) {
             ++lp;
             loff = 0;
-            lpage = __ldg(a.block_table + (int64_t)lb * a.max_pages + lp);
+            lpage = lnext;
+            lnext = page(lp + 1);
         }
         Tile x{0, 0};
         if (lpage >= 0 && lpage < a.n_pages) {
@@ -541,8 +606,13 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
             x.blk = row >> a.block_log2;
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar + at, 2 * kTile * D);
-                bulk_load(ring[at].k, a.K_pages + (int64_t)row * D, kTile * D, bar + at);
-                bulk_load(ring[at].v, a.V_pages + (int64_t)row * D, kTile * D, bar + at);
+                if constexpr (D == 128) {
+                    tile_load(ring[at].k, &kmap, row, bar + at);
+                    tile_load(ring[at].v, &vmap, row, bar + at);
+                } else {
+                    bulk_load(ring[at].k, a.K_pages + (int64_t)row * D, kTile * D, bar + at);
+                    bulk_load(ring[at].v, a.V_pages + (int64_t)row * D, kTile * D, bar + at);
+                }
             }
         } else if (lane == 0) {
             mbar_arrive(bar + at);  // nothing to wait for
@@ -583,7 +653,7 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
         if (!__all_sync(0xffffffffu, alive)) break;  // flagged; nothing waits for the rest
         const int valid = tile[0].valid;
         if (valid > 0)
-            h.add(ring[at], tk < valid, tk + 2 < valid, ks, ks, vs, vs, valid < kTile, valid, lane);
+            h.add(ring[at], tk < valid, tk + 8 < valid, ks, ks, vs, vs, valid < kTile, valid, lane);
         ks = ks1;
         vs = vs1;
 #pragma unroll
@@ -632,30 +702,32 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, kCl ? 2 : 4) k_
         w = t = (blockIdx.x % a.cluster * (kClThreads / 32) + warp) * per;
         w_end = min64(t + per, n);
     } else {
-        const int64_t total = n * a.B * a.H_q, per = (total + a.warps - 1) / a.warps;
-        w = wi * per;
-        w_end = min64(w + per, total);
+        const Runs runs(a, n * a.B * a.H_q);
+        w = runs.begin(wi);
+        w_end = runs.end(wi);
         if (w >= w_end) return;
-        r = w / n;
-        t = w % n;
+        r = quot(w, n);
+        t = w - r * n;
     }
-    const int tk = 4 * (gid >> 1) + (gid & 1);
+    const int tk = Frag<D>::key_token(gid);
 
     // entries run kStages tiles ahead of the arithmetic, copies one less
-    int64_t ir = r, it = t, iw = w;
+    const int32_t* ip = a.idx + r * a.k + t * kTile + (lane & 15);
+    int64_t il = a.k - t * kTile, iw = w_end - w;  // entries left of the row, tiles left of the run
     auto entry = [&]() -> int {
-        if (iw >= w_end) return -1;
-        const int64_t e = it * kTile + (lane & 15);
-        const int j = e < a.k ? __ldg(a.idx + ir * a.k + e) : -1;
-        ++iw;
-        if (++it == n) {
-            it = 0;
-            ++ir;
+        if (iw-- <= 0) return -1;
+        const int j = (lane & 15) < il ? __ldg(ip) : -1;
+        if (il <= kTile) {  // on to the next row
+            ip += il;
+            il = a.k;
+        } else {
+            ip += kTile;
+            il -= kTile;
         }
         return j;
     };
-    int64_t lr = r, lt = t;
-    int lb = (int)(r / a.H_q), lhk = (int)(r % a.H_q) / G, llen = (int)q8_len(a, lb);
+    int64_t lt = n - t;  // tiles left of the copies' row
+    int lb = (int)r / a.H_q, lh = (int)r % a.H_q, lhk = lh / G, llen = (int)q8_len(a, lb);
     // issues the copies of the tile with entries j; a bit for each that counts
     auto load = [&](PickStage<D>& x, int j) -> uint32_t {
         uint32_t row = kNoRow;
@@ -675,22 +747,22 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, kCl ? 2 : 4) k_
             else copy_async<4>(x.vs + (lane - kTile), a.v_scales + blk, on);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t rr = __shfl_sync(0xffffffffu, row, tk + 2 * i);
+                const uint32_t rr = __shfl_sync(0xffffffffu, row, tk + 8 * i);
                 x.put_key(i, a.K_pages + (rr != kNoRow ? (int64_t)rr * D : 0), rr != kNoRow, lane);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t rr = __shfl_sync(0xffffffffu, row, 4 * tig + i);
+                const uint32_t rr = __shfl_sync(0xffffffffu, row, Frag<D>::value_token(i, tig));
                 x.put_value(i, a.V_pages + (rr != kNoRow ? (int64_t)rr * D : 0), rr != kNoRow, lane);
             }
         }
-        if (++lt == n) {
-            lt = 0;
-            if (++lr < (int64_t)a.B * a.H_q) {
-                lb = (int)(lr / a.H_q);
-                lhk = (int)(lr % a.H_q) / G;
-                llen = (int)q8_len(a, lb);
+        if (--lt == 0) {
+            lt = n;
+            if (++lh == a.H_q) {
+                lh = 0;
+                if (++lb < a.B) llen = (int)q8_len(a, lb);
             }
+            lhk = lh / G;
         }
         return ok;
     };
@@ -717,7 +789,7 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, kCl ? 2 : 4) k_
         copy_commit();
         if (ok[0] != 0) {
             const PickStage<D>& x = ring[at];
-            h.add(x, (ok[0] >> tk) & 1u, (ok[0] >> (tk + 2)) & 1u, x.ks[tk], x.ks[tk + 2], x.vs[tk], x.vs[tk + 2],
+            h.add(x, (ok[0] >> tk) & 1u, (ok[0] >> (tk + 8)) & 1u, x.ks[tk], x.ks[tk + 8], x.vs[tk], x.vs[tk + 8],
                   false, kTile, lane);
         }
 #pragma unroll
@@ -738,75 +810,84 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, kCl ? 2 : 4) k_
     if constexpr (kCl) merge_cluster<E>(a, h, smem, r, 1);
 }
 
-// Merges the partials of one (sequence, query head) row: the warps take
+// Merges the partials of one (sequence, query head) row: the W warps take
 // partials in turn, four columns a lane. Rows that one warp owned whole are
 // written already; rows without tokens get zeros.
-template <class E, int D>
-__global__ void __launch_bounds__(128) k_q8_combine(const AttendQ8Args a) {
-    __shared__ float sm_m[4], sm_l[4];
-    __shared__ float4 sm_acc[4][32];
+template <class E, int D, int W>
+__global__ void __launch_bounds__(32 * W) k_q8_combine(const AttendQ8Args a) {
+    __shared__ float sm_m[W], sm_l[W];
+    __shared__ float4 sm_acc[W][32];
     const int64_t r = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    griddep_wait();  // every block: the grid must not end before the partials' writers
-    int64_t unit = r, first, last, per;
+    int64_t unit = r, first, n, total;
     int Gc = 1, g = 0;
     if (a.idx != nullptr) {
-        const int64_t n = (a.k + kTile - 1) / kTile;
-        per = (n * a.B * a.H_q + a.warps - 1) / a.warps;
+        n = (a.k + kTile - 1) / kTile;
+        total = n * a.B * a.H_q;
         first = r * n;
-        last = first + n - 1;
     } else {
         Gc = a.H_q / a.H_kv;
         const int b = (int)(r / a.H_q), h = (int)(r % a.H_q);
-        int64_t before, total;
+        int64_t before;
         q8_tiles(a, b, &before, &total);
-        const int64_t n = (q8_len(a, b) + kTile - 1) / kTile;
-        if (n == 0) {
-            if (threadIdx.x < D) static_cast<typename E::T*>(a.out)[r * D + threadIdx.x] = E::from_float(0.f);
-            return;
-        }
-        per = (total * a.H_kv + a.warps - 1) / a.warps;
+        total *= a.H_kv;
+        n = (q8_len(a, b) + kTile - 1) / kTile;
         g = h % Gc;
         unit = (int64_t)b * a.H_kv + h / Gc;
         first = before * a.H_kv + (h / Gc) * n;
-        last = first + n - 1;
     }
-    const int64_t c0 = first / per;
-    const int np = (int)(last / per - c0 + 1);
-    if (np == 1 && first % per + (last - first) < per) return;
+    const Runs runs(a, total);
+    const int64_t c0 = runs.owner(first);
+    const int np = n == 0 ? 0 : (int)(runs.owner(first + n - 1) - c0 + 1);
+    griddep_wait();  // every block: the grid must not end before the partials' writers
+    if (np == 1) return;
     const float2* ml = slot_ml(a, unit + c0, Gc) + g;
-    const float* pa = slot_cols(a, unit + c0, Gc) + g * D;
-    float M = -INFINITY;
-    for (int p = threadIdx.x; p < np; p += 128) M = fmaxf(M, ml[(int64_t)p * Gc].x);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    if (lane == 0) sm_m[warp] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-    float L = 0.f;
+    const float* pa = slot_cols(a, unit + c0, Gc) + g * D + lane * 4;
+    float M = kLeast, L = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool on = lane * 4 < D;
-#pragma unroll 4
-    for (int p = warp; p < np; p += 4) {
-        const float2 x = ml[(int64_t)p * Gc];
-        const float s = x.x == -INFINITY ? 0.f : exp2f(x.x - M);
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) y = *reinterpret_cast<const float4*>(pa + (int64_t)p * Gc * D + lane * 4);
-        L += x.y * s;
-        A.x = fmaf(y.x, s, A.x);
-        A.y = fmaf(y.y, s, A.y);
-        A.z = fmaf(y.z, s, A.z);
-        A.w = fmaf(y.w, s, A.w);
+    for (int p0 = warp; p0 < np; p0 += 4 * W) {
+        float2 x[4];
+        float4 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + i * W;
+            x[i] = p < np ? ml[(int64_t)p * Gc] : make_float2(kLeast, 0.f);
+            y[i] = p < np && on ? *reinterpret_cast<const float4*>(pa + (int64_t)p * Gc * D) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float m = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), M), keep = exp2f(M - m);
+        L *= keep;
+        A = make_float4(A.x * keep, A.y * keep, A.z * keep, A.w * keep);
+        M = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float s = exp2f(x[i].x - m);
+            L = fmaf(x[i].y, s, L);
+            A.x = fmaf(y[i].x, s, A.x);
+            A.y = fmaf(y[i].y, s, A.y);
+            A.z = fmaf(y[i].z, s, A.z);
+            A.w = fmaf(y[i].w, s, A.w);
+        }
     }
     sm_acc[warp][lane] = A;
-    if (lane == 0) sm_l[warp] = L;
+    if (lane == 0) {
+        sm_m[warp] = M;
+        sm_l[warp] = L;
+    }
     __syncthreads();
     const int c = threadIdx.x;
     if (c >= D) return;
-    L = sm_l[0] + sm_l[1] + sm_l[2] + sm_l[3];
+    M = sm_m[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) M = fmaxf(M, sm_m[i]);
+    L = 0.f;
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s += reinterpret_cast<const float*>(sm_acc[i])[c];
+    for (int i = 0; i < W; ++i) {
+        const float f = exp2f(sm_m[i] - M);
+        L = fmaf(sm_l[i], f, L);
+        s = fmaf(reinterpret_cast<const float*>(sm_acc[i])[c], f, s);
+    }
     static_cast<typename E::T*>(a.out)[r * D + c] = E::from_float(L == 0.f ? 0.f : s / L);
 }
 
@@ -816,7 +897,7 @@ __global__ void __launch_bounds__(128) k_q8_combine(const AttendQ8Args a) {
 // every unit, numbered unit + warp, which grows along the line of tiles
 // (an even number: the columns behind the (m, l) pairs start on 16 bytes)
 static int64_t q8_slots(int64_t units, int64_t tiles) {
-    return (units + min64(kQ8MaxWarps, tiles) + 1) & ~(int64_t)1;
+    return (units + min64(kQ8MaxWarps, 2 * tiles) + 1) & ~(int64_t)1;
 }
 
 static size_t q8_ws_bytes(int64_t units, int64_t tiles, int G, int D) {
@@ -833,6 +914,13 @@ size_t sparse_q8_ws_bytes(int B, int H_q, int64_t k, int D) {
     return q8_ws_bytes(rows, rows * ((k + kTile - 1) / kTile), 1, D);
 }
 
+// the kernel's dynamic shared memory and the largest shared split, set once
+static cudaError_t allow_smem(const void* f, size_t bytes) {
+    const cudaError_t e = prefer_carveout(f, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess || bytes <= 48 * 1024) return e;
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 // CTAs of a cluster: as many as keep all clusters resident together, while
 // every warp has a tile. 0: too many tiles a warp, the two-kernel form.
 static int cluster_size(int64_t units, int64_t tiles, int64_t resident) {
@@ -840,6 +928,26 @@ static int cluster_size(int64_t units, int64_t tiles, int64_t resident) {
     int c = 8;
     while (c > 1 && (units * c > resident || (c / 2) * W >= tiles)) c >>= 1;
     return (tiles + c * W - 1) / (c * W) <= kClusterTiles ? c : 0;
+}
+
+// the pages as a [rows, 128] byte matrix, in boxes of one tile
+static cudaError_t page_map(CUtensorMap* m, const void* p, int64_t rows) {
+    static const PFN_cuTensorMapEncodeTiled encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (PFN_cuTensorMapEncodeTiled)f;
+    }();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, strides[1] = {128};
+    const cuuint32_t box[2] = {128, kTile}, step[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
 }
 
 template <class E, int D>
@@ -852,24 +960,28 @@ static cudaError_t attend_impl(AttendQ8Args& a, cudaStream_t s) {
     const int64_t units = sparse ? (int64_t)a.B * a.H_q : (int64_t)a.B * a.H_kv;
     const int64_t items = sparse ? a.k : (int64_t)a.page_size * a.max_pages;
     const int64_t tiles = (items + kTile - 1) / kTile;
-    auto size = [=](const void* f, int threads, size_t* smem) {
-        *smem = (size_t)threads / 32 * kStages * (sparse ? sizeof(PickStage<D>) : sizeof(PageStage<D>));
-        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)*smem);
-    };
-    size_t smem;
-    auto ck = sparse   ? k_sparse_q8<E, D, true>
-              : G <= 4 ? k_dense_q8<E, D, 1, true>
-                       : k_dense_q8<E, D, 2, true>;
-    e = size((const void*)ck, kClThreads, &smem);
-    if (e != cudaSuccess) return e;
-    a.cluster = cluster_size(units, tiles, (int64_t)di.sm_count * occupancy((const void*)ck, kClThreads, smem));
-    if (a.cluster > 0 && units * a.cluster <= 0x7fffffff) {
-        e = prefer_carveout((const void*)ck, cudaSharedmemCarveoutMaxShared);
+    CUtensorMap kmap = {}, vmap = {};
+    if (!sparse && D == 128) {
+        const int64_t rows = a.n_pages * a.H_kv * a.page_size;
+        e = page_map(&kmap, a.K_pages, rows);
+        if (e == cudaSuccess) e = page_map(&vmap, a.V_pages, rows);
         if (e != cudaSuccess) return e;
+    }
+    auto smem_of = [=](int threads) {
+        return threads / 32 * kStages * (sparse ? sizeof(PickStage<D>) : sizeof(PageStage<D>)) + (sparse ? 0 : 1024);
+    };
+    const size_t csmem = smem_of(kClThreads), smem = smem_of(kQ8Threads);
+    const void* ck = sparse   ? (const void*)k_sparse_q8<E, D, true>
+                     : G <= 4 ? (const void*)k_dense_q8<E, D, 1, true>
+                              : (const void*)k_dense_q8<E, D, 2, true>;
+    e = allow_smem(ck, csmem);
+    if (e != cudaSuccess) return e;
+    a.cluster = cluster_size(units, tiles, (int64_t)di.sm_count * occupancy(ck, kClThreads, csmem));
+    if (a.cluster > 0 && units * a.cluster <= 0x7fffffff) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(units * a.cluster));
         cfg.blockDim = dim3(kClThreads);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = csmem;
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -878,21 +990,31 @@ static cudaError_t attend_impl(AttendQ8Args& a, cudaStream_t s) {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, ck, a);
+        void* args[] = {&a, &kmap, &vmap};
+        return cudaLaunchKernelExC(&cfg, ck, args);
     }
-    auto kern = sparse   ? k_sparse_q8<E, D, false>
-                : G <= 4 ? k_dense_q8<E, D, 1, false>
-                         : k_dense_q8<E, D, 2, false>;
-    e = size((const void*)kern, kQ8Threads, &smem);
+    const void* kern = sparse   ? (const void*)k_sparse_q8<E, D, false>
+                       : G <= 4 ? (const void*)k_dense_q8<E, D, 1, false>
+                                : (const void*)k_dense_q8<E, D, 2, false>;
+    e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
     const int wpc = kQ8Threads / 32;
-    int64_t warps = (int64_t)di.sm_count * occupancy((const void*)kern, kQ8Threads, smem) * wpc;
-    warps = min64(min64(warps, kQ8MaxWarps), units * tiles);
+    int64_t warps = (int64_t)di.sm_count * occupancy(kern, kQ8Threads, smem) * wpc;
+    warps = 2 * min64(min64(warps, kQ8MaxWarps / 2), units * tiles);
     a.warps = (int)warps;
     a.slots = q8_slots(units, units * tiles);
-    e = launch_kernel(kern, dim3((unsigned)((warps + wpc - 1) / wpc)), dim3(kQ8Threads), smem, s, false, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((warps + wpc - 1) / wpc));
+    cfg.blockDim = dim3(kQ8Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    void* args[] = {&a, &kmap, &vmap};
+    e = cudaLaunchKernelExC(&cfg, kern, args);
     if (e != cudaSuccess) return e;
-    return launch_kernel(k_q8_combine<E, D>, dim3((unsigned)((int64_t)a.B * a.H_q)), dim3(128), 0, s, true, a);
+    // partials of a unit: a warp to each, within limits
+    const bool many = warps > 16 * units;
+    return launch_kernel(many ? k_q8_combine<E, D, 16> : k_q8_combine<E, D, 4>,
+                         dim3((unsigned)((int64_t)a.B * a.H_q)), dim3(many ? 512 : 128), 0, s, true, a);
 }
 
 cudaError_t launch_attend_q8(Dt out_dt, AttendQ8Args a, cudaStream_t s) {
