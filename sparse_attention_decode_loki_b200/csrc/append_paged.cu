@@ -7,169 +7,212 @@
 namespace loki {
 
 // ---------------------------------------------------------------------------
-// Streams: keys (no basis), values and queries, one read and one write of each
-// row. Bytes bound them.
+// Streams: keys (no basis), values and queries of longer appends, one read and
+// one write of each row. Bytes bound them.
 //
-// A warp takes an aligned run of 16 tokens of one head: eight lanes to a row
-// (16 columns each), four rows at a time, all loads issued before the first
-// use. 8-bit scale blocks of more than 16 tokens belong to block / 16
-// neighbouring warps, which share their largest magnitude through shared
-// memory; so every scale has one owner and every row is read once. Warps side
-// by side take the heads of one run, whose rows of the angle table they share
-// in the L1.
+// A CTA takes an aligned run of 128 positions of a sequence and goes through
+// some of its heads, keys, then values, then queries; a warp has 16 of the
+// positions, eight lanes to a row (16 columns each). The run's rows of the
+// angle table are read once, into shared memory; the next head's rows are on
+// their way while this head's are worked on, in registers. 8-bit scale blocks
+// of more than 16 tokens belong to neighbouring warps, which share their
+// largest magnitude through shared memory; so every scale has one owner.
 
-constexpr int kStThreads = 256;
+constexpr int kStThreads = 256, kStRows = 128;
 
-enum { kKindKeys, kKindValues, kKindQueries };
+template <class E>
+struct RowRegs {
+    Chunk<E> a[4], b[4];
+};
 
 template <class E, bool kQ8>
-__global__ void __launch_bounds__(kStThreads, 2) k_append_stream(const AppendArgs a) {
+__global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_stream(const AppendArgs a) {
     using Tp = typename E::T;
-    __shared__ float red[kStThreads / 32];
+    extern __shared__ __align__(16) float angles[];  // [128][rot_dim]
+    __shared__ float red[2][kStThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int gw = kQ8 ? a.block >> 4 : 1;  // warps of a task
-    const int u = lane & 7;
+    const int u = lane & 7, sub = lane >> 3;
     const bool lane_on = u < a.D >> 4;
-    int64_t task = ((int64_t)blockIdx.x * (kStThreads / 32) + warp) / gw;
-    const int sub = warp & (gw - 1);
-    int kind = kKindKeys, heads = a.H_kv;
-    if (task >= a.key_tasks) {
-        task -= a.key_tasks;
-        kind = kKindValues;
-        if (task >= a.value_tasks) {
-            task -= a.value_tasks;
-            kind = kKindQueries;
-            heads = a.H_q;
-        }
-    }
-    const bool on = task < (kind == kKindKeys ? a.key_tasks : kind == kKindValues ? a.value_tasks : a.query_tasks);
-    const int h = (int)(task % heads);
-    const int64_t rest = task / heads;
+    const int chunk = blockIdx.x % a.chunks;
+    const int64_t rest = blockIdx.x / a.chunks;
     const int b = (int)(rest % a.B);
-    const int64_t ri = rest / a.B;  // which run of the sequence's
-    const int run = 16 * gw;
-    float x[4][16];
-    int row[4];
-    bool live[4];
-    float amax = 0.f, old = 0.f;
-    int64_t first = 0, start = 0, j0 = 0;
-    bool any = false, has_old = false;
-    int block_row = -1, ca = 0, cb = 0;
-    if (on) {
-        ApSeq sq = append_seq(a, b, kind == kKindValues && ri == 0 && lane == 0 && sub == 0);
-        if (kind == kKindQueries) {  // not bound to the cache's places
-            int64_t n = a.new_lens != nullptr ? __ldg(a.new_lens + b) : a.T;
-            n = n > a.T ? a.T : n;
-            sq.hi = sq.p0 + n;
-            if (a.rope != nullptr && a.n_pos < sq.hi) sq.hi = a.n_pos;
+    const int keys = a.P == nullptr ? a.H_kv : 0, kv = keys + a.H_kv, all = kv + (a.q != nullptr ? a.H_q : 0);
+    int item = chunk * a.group;
+    const int item_end = min(item + a.group, all);
+
+    const ApSeq sq = append_seq(a, b, chunk == 0 && rest < a.B && threadIdx.x == 0);
+    int64_t qhi = a.new_lens != nullptr ? __ldg(a.new_lens + b) : a.T;  // queries need no place in the cache
+    qhi = sq.p0 + (qhi > a.T ? a.T : qhi);
+    if (a.rope != nullptr && a.n_pos < qhi) qhi = a.n_pos;
+    const int64_t start = (sq.lo / kStRows + rest / a.B) * kStRows, j0 = start + 16 * warp;
+    const int64_t top = sq.hi > qhi ? sq.hi : qhi;
+    if (start < top) {  // uniform over the CTA
+        const int rot = a.rope != nullptr ? a.rot_dim : 0;
+        if (rot > 0 && (item < keys || item_end > kv)) {
+            const int n = (int)min64(top - start, kStRows) * (rot >> 2);
+            const int skip = (int)(sq.lo > start ? sq.lo - start : 0) * (rot >> 2);
+            for (int i = skip + threadIdx.x; i < n; i += kStThreads)
+                reinterpret_cast<float4*>(angles)[i] = __ldg(reinterpret_cast<const float4*>(a.rope + start * rot) + i);
         }
-        first = sq.lo;
-        start = (sq.lo / run + ri) * run;
-        j0 = start + sub * 16;
-        const void* src = kind == kKindKeys ? a.K_new : kind == kKindValues ? a.V_new : a.q;
-        const Tp* rows = static_cast<const Tp*>(src) + ((int64_t)b * heads + h) * a.T * a.D;
-        const bool turn = kind != kKindValues && a.rope != nullptr && u < a.rot_dim >> 4;
-        unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
-        Chunk<E> wa[4], wb[4];
+        // rows of this warp in the pool, but for the head's offset (all heads' pages are the same)
+        const int gw = kQ8 ? a.block >> 4 : 1;
+        const int64_t block_start = kQ8 ? j0 & ~(int64_t)(a.block - 1) : 0;
+        int row[4] = {-1, -1, -1, -1}, block_row = -1;
+        const bool has_old = kQ8 && sq.lo > block_start;
+        if (kQ8) {  // one page holds the whole block
+            if (block_start < sq.hi && block_start + a.block > sq.lo) block_row = pool_row(a, b, 0, (int)block_start);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t j = j0 + 4 * i + (lane >> 3);
-            live[i] = lane_on && j >= sq.lo && j < sq.hi;
-            if (live[i]) {
-                const Tp* p = rows + (j - sq.p0) * a.D;
-                wa[i].load(p + ca);
-                wb[i].load(p + cb);
+            for (int i = 0; i < 4; ++i) {
+                const int64_t j = j0 + 4 * i + sub;
+                if (j >= sq.lo && j < sq.hi) row[i] = pool_row(a, b, 0, (int)j);
             }
         }
-        any = start < sq.hi && start + run > sq.lo;
-        if (kind != kKindQueries) {
-            if constexpr (kQ8) {  // one page holds the whole block
-                if (any && j0 < (int64_t)a.page_size * a.max_pages) {
-                    block_row = pool_row(a, b, h, (int)start);
-                    has_old = first > start;
-                    if (block_row >= 0 && has_old)
-                        old = (kind == kKindKeys ? a.k_scales : a.v_scales)[block_row >> a.block_log2];
-                }
+        const int64_t t0 = j0 - sq.p0 + sub;  // token of this lane's first row
+        uint32_t live_kv = 0, live_q = 0;     // bit i: its row i counts
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t j = j0 + 4 * i + sub;
+            if (lane_on && j >= sq.lo && j < sq.hi) live_kv |= 1u << i;
+            if (lane_on && j >= sq.lo && j < qhi) live_q |= 1u << i;
+        }
+        int ka, kb;  // the unit's columns where it is turned
+        unit_cols(u < rot >> 4 ? rot : 0, a.interleaved, u, &ka, &kb);
+
+        auto load = [&](RowRegs<E>& r, int it) {
+            const Tp* p;
+            if (it < kv) {
+                const int h = it < keys ? it : it - keys;
+                p = static_cast<const Tp*>(it < keys ? a.K_new : a.V_new) + ((int64_t)b * a.H_kv + h) * a.T * a.D;
             } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    row[i] = live[i] ? pool_row(a, b, h, (int)(j0 + 4 * i + (lane >> 3))) : -1;
+                p = static_cast<const Tp*>(a.q) + ((int64_t)b * a.H_q + (it - kv)) * a.T * a.D;
             }
-        }
+            const bool plain = it >= keys && it < kv;
+            const int ca = plain ? 16 * u : ka, cb = plain ? 16 * u + 8 : kb;
+            const uint32_t live = it < kv ? live_kv : live_q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!live[i]) continue;
-            const int64_t j = j0 + 4 * i + (lane >> 3);
-            if (kind == kKindValues && !kQ8) {  // values in their own type: copied, bit by bit
-                if (row[i] < 0) continue;
-                Tp* o = static_cast<Tp*>(a.V_pages) + (int64_t)row[i] * a.D;
-#pragma unroll
-                for (int e = 0; e < Chunk<E>::kN; ++e) {
-                    reinterpret_cast<uint4*>(o + ca)[e] = wa[i].w[e];
-                    reinterpret_cast<uint4*>(o + cb)[e] = wb[i].w[e];
+            for (int i = 0; i < 4; ++i)
+                if (live >> i & 1u) {
+                    r.a[i].load(p + (t0 + 4 * i) * a.D + ca);
+                    r.b[i].load(p + (t0 + 4 * i) * a.D + cb);
                 }
-                continue;
+        };
+        int parity = 0;
+        auto work = [&](const RowRegs<E>& r, int it) {
+            const bool plain = it >= keys && it < kv;
+            const int ca = plain ? 16 * u : ka, cb = plain ? 16 * u + 8 : kb;
+            const bool turn = !plain && u < rot >> 4;
+            float amax = 0.f;
+            // 8 bits: a row is turned twice, for its magnitude and for its codes; kept, the turned
+            // rows would take the registers of the loads in flight
+            auto turned = [&](int i, float* x) {
+                r.a[i].get(x);
+                r.b[i].get(x + 8);
+                if (turn) turn_unit_from(angles + (16 * warp + 4 * i + sub) * rot, rot, a.interleaved, u, x);
+            };
+            if (it >= kv) {
+                Tp* o = static_cast<Tp*>(a.q_out) + (((int64_t)b * a.H_q + (it - kv)) * a.T + t0) * a.D;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!(live_q >> i & 1u)) continue;
+                    float x[16];
+                    turned(i, x);
+                    store_chunk<E>(o + 4 * i * a.D + ca, x, ca, a.D);
+                    store_chunk<E>(o + 4 * i * a.D + cb, x + 8, cb, a.D);
+                }
+                return;
             }
-            wa[i].get(x[i]);
-            wb[i].get(x[i] + 8);
-            if (turn) turn_unit(a.rope, a.rot_dim, a.interleaved, j, u, x[i]);
-            if (kind == kKindQueries) {
-                Tp* o = static_cast<Tp*>(a.q_out) + (((int64_t)b * heads + h) * a.T + (j - sq.p0)) * a.D;
-                store_chunk<E>(o + ca, x[i], ca, a.D);
-                store_chunk<E>(o + cb, x[i] + 8, cb, a.D);
-                continue;
-            }
-            const int64_t r = kQ8 ? (block_row < 0 ? -1 : block_row + (j - start)) : row[i];
-            if (r < 0) continue;
-            if (!kQ8) {
-                Tp* o = static_cast<Tp*>(a.K_pages) + r * a.D;
-                store_chunk<E>(o + ca, x[i], ca, a.D);
-                store_chunk<E>(o + cb, x[i] + 8, cb, a.D);
-            }
-            if (kind == kKindKeys && a.plane != nullptr) {
-                Tp* o = static_cast<Tp*>(a.plane) + r * a.d_lo;
-                store_chunk<E>(o + ca, x[i], ca, a.d_lo);
-                store_chunk<E>(o + cb, x[i] + 8, cb, a.d_lo);
+            const int h = it < keys ? it : it - keys;
+            const int shift = h * a.page_size;
+            float* scales = plain ? a.v_scales : a.k_scales;
+            float old = 0.f;
+            if (kQ8 && block_row >= 0 && has_old) old = scales[(block_row + shift) >> a.block_log2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!(live_kv >> i & 1u)) continue;
+                const int64_t at = kQ8 ? (block_row < 0 ? -1 : block_row + shift + (j0 - block_start) + 4 * i + sub)
+                                       : (row[i] < 0 ? -1 : row[i] + shift);
+                if (at < 0) continue;
+                if (plain && !kQ8) {  // values in their own type: copied, bit by bit
+                    Tp* o = static_cast<Tp*>(a.V_pages) + at * a.D;
+#pragma unroll
+                    for (int e = 0; e < Chunk<E>::kN; ++e) {
+                        reinterpret_cast<uint4*>(o + ca)[e] = r.a[i].w[e];
+                        reinterpret_cast<uint4*>(o + cb)[e] = r.b[i].w[e];
+                    }
+                    continue;
+                }
+                float x[16];
+                turned(i, x);
+                if (!kQ8) {
+                    Tp* o = static_cast<Tp*>(a.K_pages) + at * a.D;
+                    store_chunk<E>(o + ca, x, ca, a.D);
+                    store_chunk<E>(o + cb, x + 8, cb, a.D);
+                }
+                if (!plain && a.plane != nullptr) {
+                    Tp* o = static_cast<Tp*>(a.plane) + at * a.d_lo;
+                    store_chunk<E>(o + ca, x, ca, a.d_lo);
+                    store_chunk<E>(o + cb, x + 8, cb, a.d_lo);
+                }
+                if constexpr (kQ8) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+                }
             }
             if constexpr (kQ8) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[i][e]));
-            }
-        }
-        if constexpr (kQ8) {
+                for (int off = 16; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                if (gw > 1) {
+                    if (lane == 0) red[parity][warp] = amax;
+                    __syncthreads();  // and every warp has read the old scale
+                    for (int w = warp & ~(gw - 1); w < (warp & ~(gw - 1)) + gw; ++w) amax = fmaxf(amax, red[parity][w]);
+                    parity ^= 1;
+                } else {
+                    __syncwarp();
+                }
+                if (block_row < 0) return;
+                const float grown = pow2_scale(amax), s = has_old ? fmaxf(old, grown) : grown;
+                if ((warp & (gw - 1)) == 0 && lane == 0) scales[(block_row + shift) >> a.block_log2] = s;
+                uint8_t* o = static_cast<uint8_t*>(plain ? a.V_pages : a.K_pages) +
+                             (block_row + shift + (j0 - block_start) + sub) * a.D;
+                const float inv = 1.f / s;
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            if (lane == 0) red[warp] = amax;
-        }
-    }
-    if constexpr (kQ8) {
-        __syncthreads();  // and every warp has read the old scale
-        if (block_row >= 0) {
-            for (int w = warp - sub; w < warp - sub + gw; ++w) amax = fmaxf(amax, red[w]);
-            const float grown = pow2_scale(amax);
-            const float s = has_old ? fmaxf(old, grown) : grown;
-            if (sub == 0 && lane == 0)
-                (kind == kKindKeys ? a.k_scales : a.v_scales)[block_row >> a.block_log2] = s;
-            uint8_t* pages = static_cast<uint8_t*>(kind == kKindKeys ? a.K_pages : a.V_pages);
-            const float inv = 1.f / s, f = old / s;
+                for (int i = 0; i < 4; ++i) {
+                    uint8_t* oi = o + 4 * i * a.D;
+                    if (live_kv >> i & 1u) {
+                        float x[16];
+                        turned(i, x);
+                        const uint2 ya = codes8(x, inv), yb = codes8(x + 8, inv);
+                        if (cb == ca + 8) {
+                            *reinterpret_cast<uint4*>(oi + ca) = make_uint4(ya.x, ya.y, yb.x, yb.y);
+                        } else {
+                            *reinterpret_cast<uint2*>(oi + ca) = ya;
+                            *reinterpret_cast<uint2*>(oi + cb) = yb;
+                        }
+                    } else if (lane_on && has_old && s > old && j0 + 4 * i + sub < sq.lo) {  // older codes to the new scale
+                        const float f = old / s;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t j = j0 + 4 * i + (lane >> 3);
-                uint8_t* o = pages + (block_row + (j - start)) * a.D;
-                if (live[i]) {
-                    *reinterpret_cast<uint2*>(o + ca) = codes8(x[i], inv);
-                    *reinterpret_cast<uint2*>(o + cb) = codes8(x[i] + 8, inv);
-                } else if (lane_on && has_old && s > old && j < first) {  // older codes to the new scale
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint2* w = reinterpret_cast<uint2*>(o + (e ? cb : ca));
-                        uint2 v = *w;
-                        v.x = rescale4(v.x, f);
-                        v.y = rescale4(v.y, f);
-                        *w = v;
+                        for (int e = 0; e < 2; ++e) {
+                            uint2* w = reinterpret_cast<uint2*>(oi + (e ? cb : ca));
+                            uint2 v = *w;
+                            v.x = rescale4(v.x, f);
+                            v.y = rescale4(v.y, f);
+                            *w = v;
+                        }
                     }
                 }
             }
+        };
+        RowRegs<E> r0, r1;
+        load(r0, item);
+        __syncthreads();  // the angles
+        while (true) {
+            if (item + 1 < item_end) load(r1, item + 1);
+            work(r0, item);
+            if (++item >= item_end) break;
+            if (item + 1 < item_end) load(r0, item + 1);
+            work(r1, item);
+            if (++item >= item_end) break;
         }
     }
     // as a programmatic dependent of the keys' kernel: end after it
@@ -177,14 +220,14 @@ __global__ void __launch_bounds__(kStThreads, 2) k_append_stream(const AppendArg
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens (a decode step) against the basis. Latency bounds it: one CTA
-// per KV head and group of sequences, at most 16 rows. A quarter of a basis
-// column sits in each thread's registers, loaded before anything else; a warp
-// per row turns it, quantises it and stores it.
+// Few tokens (a decode step), with or without a basis. Latency bounds it: one
+// CTA per KV head and group of sequences, at most 16 rows. A quarter of a
+// basis column sits in each thread's registers, loaded before anything else;
+// a warp per row turns it, quantises it and stores it.
 
 constexpr int kRwThreads = 512, kRwRows = 16;
 
-template <class E, bool kQ8, int D>
+template <class E, bool kQ8, int D, bool kBasis>
 __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) {
     using Tp = typename E::T;
     constexpr int DQ = D / 4;
@@ -221,7 +264,7 @@ __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) 
     const int hk = blockIdx.x % a.H_kv, b0 = blockIdx.x / a.H_kv * a.group;
     const int c = threadIdx.x & 127, qd = threadIdx.x >> 7;
     float p[DQ];
-    if (c < D) {
+    if (kBasis && c < D) {
         const float* Ph = a.P + ((int64_t)hk * D + qd * DQ) * D + c;
 #pragma unroll
         for (int i = 0; i < DQ; ++i) p[i] = __ldg(Ph + i * D);
@@ -290,7 +333,7 @@ __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) 
         if (lane == 0) blk[warp] = row < 0 ? -1 : row >> a.block_log2;
     }
     __syncthreads();
-    for (int r0 = 0; r0 < rows; r0 += 8) {
+    for (int r0 = 0; kBasis && r0 < rows; r0 += 8) {
         float acc[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) acc[r] = 0.f;
@@ -429,13 +472,19 @@ __global__ void __launch_bounds__(256) k_rope_table(float* __restrict__ table, i
 
 // ---------------------------------------------------------------------------
 
+template <class E, bool kQ8, int D>
+static cudaError_t rows_impl(const AppendArgs& a, int64_t ctas, cudaStream_t s) {
+    return launch_kernel(a.P != nullptr ? k_append_rows<E, kQ8, D, true> : k_append_rows<E, kQ8, D, false>,
+                         dim3((unsigned)ctas), dim3(kRwThreads), 0, s, false, a);
+}
+
 template <class E, bool kQ8>
 static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
-    if (a.P != nullptr && a.T <= kRwRows) {
+    DevInfo di;
+    cudaError_t e = dev_info(&di);
+    if (e != cudaSuccess) return e;
+    if (a.T <= kRwRows) {
         // sequences of a CTA: as many as still leave a CTA for every SM
-        DevInfo di;
-        cudaError_t e = dev_info(&di);
-        if (e != cudaSuccess) return e;
         int64_t group = (int64_t)a.B * a.H_kv / di.sm_count;
         group = group < 1 ? 1 : group;
         group = min64(min64(group, kRwRows / a.T), a.B);
@@ -444,24 +493,27 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
         const int64_t q = a.q != nullptr ? ((int64_t)a.B * a.H_q * a.T * 8 + kRwThreads - 1) / kRwThreads : 0;
         if (kv + q > 0x7fffffff) return cudaErrorInvalidValue;
         a.kv_ctas = (int)kv;
-        auto kern = a.D == 96 ? k_append_rows<E, kQ8, 96> : k_append_rows<E, kQ8, 128>;
-        return launch_kernel(kern, dim3((unsigned)(kv + q)), dim3(kRwThreads), 0, s, false, a);
+        return a.D == 96 ? rows_impl<E, kQ8, 96>(a, kv + q, s) : rows_impl<E, kQ8, 128>(a, kv + q, s);
     }
     bool behind = false;
     if (a.P != nullptr) {
-        const cudaError_t e = launch_append_basis(E::kBytes == 4 ? kF32 : kBF16, a, s);
+        e = launch_append_basis(E::kBytes == 4 ? kF32 : kBF16, a, s);
         if (e != cudaSuccess) return e;
         behind = true;
     }
-    const int gw = kQ8 ? a.block / 16 : 1, run = 16 * gw;
-    const int64_t runs = ((int64_t)a.T + run - 2) / run + 1;
-    a.key_tasks = a.P == nullptr ? runs * a.B * a.H_kv : 0;
-    a.value_tasks = runs * a.B * a.H_kv;
-    a.query_tasks = a.q != nullptr ? runs * a.B * a.H_q : 0;
-    const int64_t per = kStThreads / 32 / gw;
-    const int64_t ctas = (a.key_tasks + a.value_tasks + a.query_tasks + per - 1) / per;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_kernel(k_append_stream<E, kQ8>, dim3((unsigned)ctas), dim3(kStThreads), 0, s, behind, a);
+    // heads of a CTA: three CTAs for every place on the device, or one head
+    const int heads = (a.P == nullptr ? 2 : 1) * a.H_kv + (a.q != nullptr ? a.H_q : 0);
+    const int64_t runs = (((int64_t)a.T + kStRows - 2) / kStRows + 1) * a.B;
+    int64_t group = runs * heads / (di.sm_count * 6);
+    group = group < 1 ? 1 : min64(group, min64(heads, 16));
+    a.group = (int)group;
+    a.chunks = (int)((heads + group - 1) / group);
+    if (runs * a.chunks > 0x7fffffff) return cudaErrorInvalidValue;
+    auto kern = k_append_stream<E, kQ8>;
+    const size_t smem = a.rope != nullptr ? (size_t)kStRows * a.rot_dim * sizeof(float) : 0;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStRows * 128 * 4);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3((unsigned)(runs * a.chunks)), dim3(kStThreads), smem, s, behind, a);
 }
 
 cudaError_t launch_append_paged(Dt dt, AppendArgs a, cudaStream_t s) {

@@ -100,31 +100,47 @@ __device__ __forceinline__ void store_chunk(typename E::T* p, const float* f, in
         if (col + i * E::kVec < limit) reinterpret_cast<uint4*>(p)[i] = pack16(f + i * E::kVec, E());
 }
 
-// the unit's columns x[0..7] (chunk a) and x[8..15] (chunk b) turned by the
-// angles of position j (u < rot_dim / 16)
-__device__ __forceinline__ void turn_unit(const float* rope, int rot_dim, int interleaved, int64_t j, int u, float* x) {
-    const float4* cp = reinterpret_cast<const float4*>(rope + j * rot_dim + 8 * u);
-    const float4* sp = reinterpret_cast<const float4*>(rope + j * rot_dim + (rot_dim >> 1) + 8 * u);
+// the angles of a unit: cos and sin of entries 8u .. 8u + 7 of a table row
+struct Angles {
     float c[8], s[8];
-    *reinterpret_cast<float4*>(c) = __ldg(cp);
-    *reinterpret_cast<float4*>(c + 4) = __ldg(cp + 1);
-    *reinterpret_cast<float4*>(s) = __ldg(sp);
-    *reinterpret_cast<float4*>(s + 4) = __ldg(sp + 1);
-    if (interleaved) {
+    // from shared or global memory
+    __device__ __forceinline__ void load(const float* row, int rot_dim, int u) {
+        const float4* cp = reinterpret_cast<const float4*>(row + 8 * u);
+        const float4* sp = reinterpret_cast<const float4*>(row + (rot_dim >> 1) + 8 * u);
+        *reinterpret_cast<float4*>(c) = cp[0];
+        *reinterpret_cast<float4*>(c + 4) = cp[1];
+        *reinterpret_cast<float4*>(s) = sp[0];
+        *reinterpret_cast<float4*>(s + 4) = sp[1];
+    }
+    // the unit's columns x[0..7] (chunk a) and x[8..15] (chunk b)
+    __device__ __forceinline__ void turn(float* x, int interleaved) const {
+        if (interleaved) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float p = x[2 * e], q = x[2 * e + 1];
-            x[2 * e] = fmaf(-q, s[e], p * c[e]);
-            x[2 * e + 1] = fmaf(p, s[e], q * c[e]);
-        }
-    } else {
+            for (int e = 0; e < 8; ++e) {
+                const float p = x[2 * e], q = x[2 * e + 1];
+                x[2 * e] = fmaf(-q, s[e], p * c[e]);
+                x[2 * e + 1] = fmaf(p, s[e], q * c[e]);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float p = x[e], q = x[e + 8];
-            x[e] = fmaf(-q, s[e], p * c[e]);
-            x[e + 8] = fmaf(p, s[e], q * c[e]);
+            for (int e = 0; e < 8; ++e) {
+                const float p = x[e], q = x[e + 8];
+                x[e] = fmaf(-q, s[e], p * c[e]);
+                x[e + 8] = fmaf(p, s[e], q * c[e]);
+            }
         }
     }
+};
+
+__device__ __forceinline__ void turn_unit_from(const float* row, int rot_dim, int interleaved, int u, float* x) {
+    Angles g;
+    g.load(row, rot_dim, u);
+    g.turn(x, interleaved);
+}
+
+// the unit turned by the angles of position j (u < rot_dim / 16)
+__device__ __forceinline__ void turn_unit(const float* rope, int rot_dim, int interleaved, int64_t j, int u, float* x) {
+    turn_unit_from(rope + j * rot_dim, rot_dim, interleaved, u, x);
 }
 
 // column c of the row at position j, turned
