@@ -7,216 +7,276 @@
 namespace loki {
 
 // ---------------------------------------------------------------------------
-// Streams: keys (no basis), values and queries of longer appends, one read and
-// one write of each row. Bytes bound them.
+// Longer appends as streams, one read and one write of each row. Bytes bound
+// them, and what the loads in flight cost is registers: values and queries
+// share a kernel of 24 warps an SM, keys without a basis, which are turned and
+// then scaled, have one of their own with 16.
 //
-// A CTA takes an aligned run of 128 positions of a sequence and goes through
-// some of its heads, keys, then values, then queries; a warp has 16 of the
-// positions, eight lanes to a row (16 columns each). The run's rows of the
-// angle table are read once, into shared memory; the next head's rows are on
-// their way while this head's are worked on, in registers. 8-bit scale blocks
-// of more than 16 tokens belong to neighbouring warps, which share their
-// largest magnitude through shared memory; so every scale has one owner.
+// Values and keys: a CTA has an aligned run of 128 positions and goes through
+// some heads, a warp has 16 of the positions, eight lanes to a row (16 columns
+// each). 8-bit scale blocks of more than 16 tokens belong to neighbouring
+// warps, which share their largest magnitude through shared memory, so every
+// scale has one owner.
+// Queries: a warp has four positions, whose angles stay in its registers while
+// it goes through the heads.
 
-constexpr int kStThreads = 256, kStRows = 128;
+constexpr int kStThreads = 256, kStQueryRows = 32;
 
-template <class E>
-struct RowRegs {
-    Chunk<E> a[4], b[4];
-};
-
-template <class E, bool kQ8>
-__global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_stream(const AppendArgs a) {
-    using Tp = typename E::T;
-    extern __shared__ __align__(16) float angles[];  // [128][rot_dim]
-    __shared__ float red[2][kStThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int u = lane & 7, sub = lane >> 3;
-    const bool lane_on = u < a.D >> 4;
-    const int chunk = blockIdx.x % a.chunks;
-    const int64_t rest = blockIdx.x / a.chunks;
-    const int b = (int)(rest % a.B);
-    const int keys = a.P == nullptr ? a.H_kv : 0, kv = keys + a.H_kv, all = kv + (a.q != nullptr ? a.H_q : 0);
-    int item = chunk * a.group;
-    const int item_end = min(item + a.group, all);
-
-    const ApSeq sq = append_seq(a, b, chunk == 0 && rest < a.B && threadIdx.x == 0);
-    int64_t qhi = a.new_lens != nullptr ? __ldg(a.new_lens + b) : a.T;  // queries need no place in the cache
-    qhi = sq.p0 + (qhi > a.T ? a.T : qhi);
-    if (a.rope != nullptr && a.n_pos < qhi) qhi = a.n_pos;
-    const int64_t start = (sq.lo / kStRows + rest / a.B) * kStRows, j0 = start + 16 * warp;
-    const int64_t top = sq.hi > qhi ? sq.hi : qhi;
-    if (start < top) {  // uniform over the CTA
-        const int rot = a.rope != nullptr ? a.rot_dim : 0;
-        if (rot > 0 && (item < keys || item_end > kv)) {
-            const int n = (int)min64(top - start, kStRows) * (rot >> 2);
-            const int skip = (int)(sq.lo > start ? sq.lo - start : 0) * (rot >> 2);
-            for (int i = skip + threadIdx.x; i < n; i += kStThreads)
-                reinterpret_cast<float4*>(angles)[i] = __ldg(reinterpret_cast<const float4*>(a.rope + start * rot) + i);
+// a warp's 16 positions of a run and their place in the pool but for the head's
+// offset (the page is the same for all heads)
+template <bool kQ8>
+struct RunPlace {
+    int64_t j0, block_start;
+    int row[kQ8 ? 1 : 4];  // 8 bits: of the scale block's first token; -1: none
+    uint32_t live;         // bit i: position j0 + 4 i + lane / 8 is appended and has a place
+    bool has_old;          // the block holds older tokens
+    __device__ __forceinline__ RunPlace(const AppendArgs& a, const ApSeq& s, int b, int64_t start, bool lane_on) {
+        const int sub = threadIdx.x >> 3 & 3;
+        j0 = start + 16 * (threadIdx.x >> 5);
+        block_start = kQ8 ? j0 & ~(int64_t)(a.block - 1) : 0;
+        has_old = kQ8 && s.lo > block_start;
+        live = 0;
+        if constexpr (kQ8) {  // one page holds the whole block
+            row[0] = block_start < s.hi && block_start + a.block > s.lo ? pool_row(a, b, 0, (int)block_start) : -1;
         }
-        // rows of this warp in the pool, but for the head's offset (all heads' pages are the same)
-        const int gw = kQ8 ? a.block >> 4 : 1;
-        const int64_t block_start = kQ8 ? j0 & ~(int64_t)(a.block - 1) : 0;
-        int row[4] = {-1, -1, -1, -1}, block_row = -1;
-        const bool has_old = kQ8 && sq.lo > block_start;
-        if (kQ8) {  // one page holds the whole block
-            if (block_start < sq.hi && block_start + a.block > sq.lo) block_row = pool_row(a, b, 0, (int)block_start);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t j = j0 + 4 * i + sub;
-                if (j >= sq.lo && j < sq.hi) row[i] = pool_row(a, b, 0, (int)j);
-            }
-        }
-        const int64_t t0 = j0 - sq.p0 + sub;  // token of this lane's first row
-        uint32_t live_kv = 0, live_q = 0;     // bit i: its row i counts
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t j = j0 + 4 * i + sub;
-            if (lane_on && j >= sq.lo && j < sq.hi) live_kv |= 1u << i;
-            if (lane_on && j >= sq.lo && j < qhi) live_q |= 1u << i;
+            const bool in = j >= s.lo && j < s.hi;
+            if constexpr (!kQ8) row[i] = in ? pool_row(a, b, 0, (int)j) : -1;
+            if (lane_on && in && row[kQ8 ? 0 : i] >= 0) live |= 1u << i;
         }
-        int ka, kb;  // the unit's columns where it is turned
-        unit_cols(u < rot >> 4 ? rot : 0, a.interleaved, u, &ka, &kb);
+    }
+    // pool row of position j0 + 4 i + lane / 8 under a head's offset
+    __device__ __forceinline__ int64_t at(int i, int shift) const {
+        return kQ8 ? row[0] + shift + (int)(j0 - block_start) + 4 * i + (int)(threadIdx.x >> 3 & 3)
+                   : row[kQ8 ? 0 : i] + shift;
+    }
+};
 
-        auto load = [&](RowRegs<E>& r, int it) {
-            const Tp* p;
-            if (it < kv) {
-                const int h = it < keys ? it : it - keys;
-                p = static_cast<const Tp*>(it < keys ? a.K_new : a.V_new) + ((int64_t)b * a.H_kv + h) * a.T * a.D;
-            } else {
-                p = static_cast<const Tp*>(a.q) + ((int64_t)b * a.H_q + (it - kv)) * a.T * a.D;
-            }
-            const bool plain = it >= keys && it < kv;
-            const int ca = plain ? 16 * u : ka, cb = plain ? 16 * u + 8 : kb;
-            const uint32_t live = it < kv ? live_kv : live_q;
+// The block's new scale from this warp's largest magnitude: shared with the
+// block's other warps through red (two sets in turn), stored by the first.
+// Every warp of the CTA calls it; old is the scale before.
+__device__ __forceinline__ float block_scale(const AppendArgs& a, float amax, float* red, float* scale, bool has_old,
+                                             float* old) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gw = a.block >> 4;
+    *old = scale != nullptr && has_old ? *scale : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (live >> i & 1u) {
-                    r.a[i].load(p + (t0 + 4 * i) * a.D + ca);
-                    r.b[i].load(p + (t0 + 4 * i) * a.D + cb);
-                }
-        };
-        int parity = 0;
-        auto work = [&](const RowRegs<E>& r, int it) {
-            const bool plain = it >= keys && it < kv;
-            const int ca = plain ? 16 * u : ka, cb = plain ? 16 * u + 8 : kb;
-            const bool turn = !plain && u < rot >> 4;
-            float amax = 0.f;
-            // 8 bits: a row is turned twice, for its magnitude and for its codes; kept, the turned
-            // rows would take the registers of the loads in flight
-            auto turned = [&](int i, float* x) {
-                r.a[i].get(x);
-                r.b[i].get(x + 8);
-                if (turn) turn_unit_from(angles + (16 * warp + 4 * i + sub) * rot, rot, a.interleaved, u, x);
-            };
-            if (it >= kv) {
-                Tp* o = static_cast<Tp*>(a.q_out) + (((int64_t)b * a.H_q + (it - kv)) * a.T + t0) * a.D;
+    for (int off = 16; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (gw > 1) {
+        if (lane == 0) red[warp] = amax;
+        __syncthreads();  // and every warp has read the old scale
+        for (int w = warp & ~(gw - 1); w < (warp & ~(gw - 1)) + gw; ++w) amax = fmaxf(amax, red[w]);
+    } else {
+        __syncwarp();
+    }
+    const float grown = pow2_scale(amax), s = has_old ? fmaxf(*old, grown) : grown;
+    if (scale != nullptr && (warp & (gw - 1)) == 0 && lane == 0) *scale = s;
+    return s;
+}
+
+// the older codes of a warp's positions, moved from scale `old` to s
+__device__ __forceinline__ void rescale_rows(const AppendArgs& a, uint8_t* codes, int64_t j0, int64_t lo, float f) {
+    const int u = threadIdx.x & 7, sub = threadIdx.x >> 3 & 3;
+    if (u >= a.D >> 4) return;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        if (j0 + 4 * i + sub >= lo) continue;
+        uint4* w = reinterpret_cast<uint4*>(codes + (4 * i + sub) * a.D + 16 * u);
+        uint4 v = *w;
+        v.x = rescale4(v.x, f);
+        v.y = rescale4(v.y, f);
+        v.z = rescale4(v.z, f);
+        v.w = rescale4(v.w, f);
+        *w = v;
+    }
+}
+
+template <class E, bool kQ8>
+__global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_stream(const AppendArgs a) {
+    using Tp = typename E::T;
+    __shared__ float red[2][kStThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
+    const bool lane_on = u < a.D >> 4;
+    if ((int)blockIdx.x >= a.kv_ctas) {
+        const int q = blockIdx.x - a.kv_ctas, chunk = q % a.q_chunks, rest = q / a.q_chunks, b = rest % a.B;
+        const int t = rest / a.B * kStQueryRows + 4 * warp + sub;
+        const int64_t j = (int64_t)__ldg(a.positions + b) + t;
+        const int n = a.new_lens != nullptr ? min(__ldg(a.new_lens + b), a.T) : a.T;
+        if (lane_on && t < n && j >= 0 && (a.rope == nullptr || j < a.n_pos)) {
+            const bool turn = a.rope != nullptr && u < a.rot_dim >> 4;
+            int ca, cb;
+            unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
+            Angles g;
+            if (turn) g.load(a.rope + j * a.rot_dim, a.rot_dim, u);
+            const int h0 = chunk * a.q_group, h1 = min(h0 + a.q_group, a.H_q);
+            const int64_t step = (int64_t)a.T * a.D, at = (((int64_t)b * a.H_q + h0) * a.T + t) * a.D;
+            const Tp* p = static_cast<const Tp*>(a.q) + at;
+            Tp* o = static_cast<Tp*>(a.q_out) + at;
+            constexpr int U = E::kBytes == 2 ? 4 : 2;
+            for (int h = h0; h < h1; h += U) {
+                Chunk<E> wa[U], wb[U];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!(live_q >> i & 1u)) continue;
-                    float x[16];
-                    turned(i, x);
-                    store_chunk<E>(o + 4 * i * a.D + ca, x, ca, a.D);
-                    store_chunk<E>(o + 4 * i * a.D + cb, x + 8, cb, a.D);
-                }
-                return;
-            }
-            const int h = it < keys ? it : it - keys;
-            const int shift = h * a.page_size;
-            float* scales = plain ? a.v_scales : a.k_scales;
-            float old = 0.f;
-            if (kQ8 && block_row >= 0 && has_old) old = scales[(block_row + shift) >> a.block_log2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (!(live_kv >> i & 1u)) continue;
-                const int64_t at = kQ8 ? (block_row < 0 ? -1 : block_row + shift + (j0 - block_start) + 4 * i + sub)
-                                       : (row[i] < 0 ? -1 : row[i] + shift);
-                if (at < 0) continue;
-                if (plain && !kQ8) {  // values in their own type: copied, bit by bit
-                    Tp* o = static_cast<Tp*>(a.V_pages) + at * a.D;
-#pragma unroll
-                    for (int e = 0; e < Chunk<E>::kN; ++e) {
-                        reinterpret_cast<uint4*>(o + ca)[e] = r.a[i].w[e];
-                        reinterpret_cast<uint4*>(o + cb)[e] = r.b[i].w[e];
+                for (int i = 0; i < U; ++i)
+                    if (h + i < h1) {
+                        wa[i].load(p + i * step + ca);
+                        wb[i].load(p + i * step + cb);
                     }
-                    continue;
-                }
-                float x[16];
-                turned(i, x);
-                if (!kQ8) {
-                    Tp* o = static_cast<Tp*>(a.K_pages) + at * a.D;
-                    store_chunk<E>(o + ca, x, ca, a.D);
-                    store_chunk<E>(o + cb, x + 8, cb, a.D);
-                }
-                if (!plain && a.plane != nullptr) {
-                    Tp* o = static_cast<Tp*>(a.plane) + at * a.d_lo;
-                    store_chunk<E>(o + ca, x, ca, a.d_lo);
-                    store_chunk<E>(o + cb, x + 8, cb, a.d_lo);
-                }
-                if constexpr (kQ8) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
-                }
-            }
-            if constexpr (kQ8) {
-#pragma unroll
-                for (int off = 16; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                if (gw > 1) {
-                    if (lane == 0) red[parity][warp] = amax;
-                    __syncthreads();  // and every warp has read the old scale
-                    for (int w = warp & ~(gw - 1); w < (warp & ~(gw - 1)) + gw; ++w) amax = fmaxf(amax, red[parity][w]);
-                    parity ^= 1;
-                } else {
-                    __syncwarp();
-                }
-                if (block_row < 0) return;
-                const float grown = pow2_scale(amax), s = has_old ? fmaxf(old, grown) : grown;
-                if ((warp & (gw - 1)) == 0 && lane == 0) scales[(block_row + shift) >> a.block_log2] = s;
-                uint8_t* o = static_cast<uint8_t*>(plain ? a.V_pages : a.K_pages) +
-                             (block_row + shift + (j0 - block_start) + sub) * a.D;
-                const float inv = 1.f / s;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint8_t* oi = o + 4 * i * a.D;
-                    if (live_kv >> i & 1u) {
+                for (int i = 0; i < U; ++i)
+                    if (h + i < h1) {
                         float x[16];
-                        turned(i, x);
-                        const uint2 ya = codes8(x, inv), yb = codes8(x + 8, inv);
-                        if (cb == ca + 8) {
-                            *reinterpret_cast<uint4*>(oi + ca) = make_uint4(ya.x, ya.y, yb.x, yb.y);
-                        } else {
-                            *reinterpret_cast<uint2*>(oi + ca) = ya;
-                            *reinterpret_cast<uint2*>(oi + cb) = yb;
-                        }
-                    } else if (lane_on && has_old && s > old && j0 + 4 * i + sub < sq.lo) {  // older codes to the new scale
-                        const float f = old / s;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint2* w = reinterpret_cast<uint2*>(oi + (e ? cb : ca));
-                            uint2 v = *w;
-                            v.x = rescale4(v.x, f);
-                            v.y = rescale4(v.y, f);
-                            *w = v;
-                        }
+                        wa[i].get(x);
+                        wb[i].get(x + 8);
+                        if (turn) g.turn(x, a.interleaved);
+                        store_chunk<E>(o + i * step + ca, x, ca, a.D);
+                        store_chunk<E>(o + i * step + cb, x + 8, cb, a.D);
                     }
+                p += U * step;
+                o += U * step;
+            }
+        }
+    } else {
+        const int chunk = blockIdx.x % a.chunks, rest = blockIdx.x / a.chunks, b = rest % a.B;
+        const ApSeq sq = append_seq(a, b, chunk == 0 && rest < a.B && threadIdx.x == 0);
+        const int64_t start = (sq.lo / kRunRows + rest / a.B) * kRunRows;
+        if (start < sq.hi) {  // uniform over the CTA
+            const RunPlace<kQ8> pl(a, sq, b, start, lane_on);
+            const int h0 = chunk * a.group, h1 = min(h0 + a.group, a.H_kv);
+            const int64_t step = (int64_t)a.T * a.D;
+            const Tp* p = static_cast<const Tp*>(a.V_new) + ((int64_t)b * a.H_kv + h0) * step +
+                          (pl.j0 - sq.p0 + sub) * a.D + 16 * u;
+            int parity = 0;
+            for (int h = h0; h < h1; ++h, p += step) {
+                const int shift = h * a.page_size;
+                Chunk<E> w[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (pl.live >> i & 1u) {
+                        w[i][0].load(p + 4 * i * a.D);
+                        w[i][1].load(p + 4 * i * a.D + 8);
+                    }
+                if constexpr (!kQ8) {  // in their own type: copied, bit by bit
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (pl.live >> i & 1u) {
+                            uint4* o = reinterpret_cast<uint4*>(static_cast<Tp*>(a.V_pages) + pl.at(i, shift) * a.D + 16 * u);
+#pragma unroll
+                            for (int e = 0; e < Chunk<E>::kN; ++e) {
+                                o[e] = w[i][0].w[e];
+                                o[Chunk<E>::kN + e] = w[i][1].w[e];
+                            }
+                        }
+                } else {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (pl.live >> i & 1u) {
+                            float x[16];
+                            w[i][0].get(x);
+                            w[i][1].get(x + 8);
+                            amax = finite_amax<16>(amax, x);
+                        }
+                    float old;
+                    float* sc = pl.row[0] < 0 ? nullptr : a.v_scales + ((pl.row[0] + shift) >> a.block_log2);
+                    const float s = block_scale(a, amax, red[parity], sc, pl.has_old, &old), inv = 1.f / s;
+                    parity ^= 1;
+                    uint8_t* o = static_cast<uint8_t*>(a.V_pages) + (pl.at(0, shift) - sub) * a.D;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (pl.live >> i & 1u) {
+                            float x[16];
+                            w[i][0].get(x);
+                            w[i][1].get(x + 8);
+                            const uint2 y = codes8(x, inv), z = codes8(x + 8, inv);
+                            *reinterpret_cast<uint4*>(o + (4 * i + sub) * a.D + 16 * u) = make_uint4(y.x, y.y, z.x, z.y);
+                        }
+                    if (sc != nullptr && pl.has_old && s > old) rescale_rows(a, o, pl.j0, sq.lo, old / s);
                 }
             }
-        };
-        RowRegs<E> r0, r1;
-        load(r0, item);
-        __syncthreads();  // the angles
-        while (true) {
-            if (item + 1 < item_end) load(r1, item + 1);
-            work(r0, item);
-            if (++item >= item_end) break;
-            if (item + 1 < item_end) load(r0, item + 1);
-            work(r1, item);
-            if (++item >= item_end) break;
         }
     }
     // as a programmatic dependent of the keys' kernel: end after it
     griddep_wait();
+}
+
+template <class E, bool kQ8>
+__global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_keys(const AppendArgs a) {
+    using Tp = typename E::T;
+    extern __shared__ __align__(16) float angles[];  // the run's, [128][rot_dim]
+    __shared__ float red[2][kStThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
+    const bool lane_on = u < a.D >> 4;
+    const int chunk = blockIdx.x % a.chunks, rest = blockIdx.x / a.chunks, b = rest % a.B;
+    griddep_launch_dependents();
+    const ApSeq sq = append_seq(a, b, false);
+    const int64_t start = (sq.lo / kRunRows + rest / a.B) * kRunRows;
+    if (start >= sq.hi) return;
+    const int rot = a.rope != nullptr ? a.rot_dim : 0;
+    if (rot > 0) {
+        const int n = (int)min64(sq.hi - start, kRunRows) * (rot >> 2);
+        const int skip = (int)(sq.lo > start ? sq.lo - start : 0) * (rot >> 2);
+        for (int i = skip + threadIdx.x; i < n; i += kStThreads)
+            reinterpret_cast<float4*>(angles)[i] = __ldg(reinterpret_cast<const float4*>(a.rope + start * rot) + i);
+    }
+    const RunPlace<kQ8> pl(a, sq, b, start, lane_on);
+    const bool turn = u < rot >> 4;
+    int ca, cb;
+    unit_cols(turn ? rot : 0, a.interleaved, u, &ca, &cb);
+    const int h0 = chunk * a.group, h1 = min(h0 + a.group, a.H_kv);
+    const int64_t step = (int64_t)a.T * a.D;
+    const Tp* p = static_cast<const Tp*>(a.K_new) + ((int64_t)b * a.H_kv + h0) * step + (pl.j0 - sq.p0 + sub) * a.D;
+    Chunk<E> wa[4], wb[4];
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (pl.live >> i & 1u) {
+                wa[i].load(p + 4 * i * a.D + ca);
+                wb[i].load(p + 4 * i * a.D + cb);
+            }
+        p += step;
+    };
+    load();
+    __syncthreads();  // the angles
+    int parity = 0;
+    for (int h = h0; h < h1; ++h) {
+        const int shift = h * a.page_size;
+        float x[4][16], amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wa[i].get(x[i]);
+            wb[i].get(x[i] + 8);
+            if (turn) turn_unit_from(angles + (16 * warp + 4 * i + sub) * rot, rot, a.interleaved, u, x[i]);
+            if (!(pl.live >> i & 1u)) continue;
+            if (a.plane != nullptr) {
+                Tp* o = static_cast<Tp*>(a.plane) + pl.at(i, shift) * a.d_lo;
+                store_chunk<E>(o + ca, x[i], ca, a.d_lo);
+                store_chunk<E>(o + cb, x[i] + 8, cb, a.d_lo);
+            }
+            if constexpr (!kQ8) {
+                Tp* o = static_cast<Tp*>(a.K_pages) + pl.at(i, shift) * a.D;
+                store_chunk<E>(o + ca, x[i], ca, a.D);
+                store_chunk<E>(o + cb, x[i] + 8, cb, a.D);
+            } else {
+                amax = finite_amax<16>(amax, x[i]);
+            }
+        }
+        if (h + 1 < h1) load();
+        if constexpr (kQ8) {
+            float old;
+            float* sc = pl.row[0] < 0 ? nullptr : a.k_scales + ((pl.row[0] + shift) >> a.block_log2);
+            const float s = block_scale(a, amax, red[parity], sc, pl.has_old, &old), inv = 1.f / s;
+            parity ^= 1;
+            uint8_t* o = static_cast<uint8_t*>(a.K_pages) + (pl.at(0, shift) - sub) * a.D;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (pl.live >> i & 1u) {
+                    *reinterpret_cast<uint2*>(o + (4 * i + sub) * a.D + ca) = codes8(x[i], inv);
+                    *reinterpret_cast<uint2*>(o + (4 * i + sub) * a.D + cb) = codes8(x[i] + 8, inv);
+                }
+            if (sc != nullptr && pl.has_old && s > old) rescale_rows(a, o, pl.j0, sq.lo, old / s);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -495,25 +555,41 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
         a.kv_ctas = (int)kv;
         return a.D == 96 ? rows_impl<E, kQ8, 96>(a, kv + q, s) : rows_impl<E, kQ8, 128>(a, kv + q, s);
     }
-    bool behind = false;
+    // keys first; values and queries run beside them as a programmatic dependent
+    const int64_t runs = (((int64_t)a.T + kRunRows - 2) / kRunRows + 1) * a.B;
+    // heads of a CTA: as many as still leave `waves` CTAs for every place on the device
+    auto heads_per_cta = [&](int64_t ctas, int heads, int per_sm, int waves) {
+        const int64_t g = ctas * heads / ((int64_t)di.sm_count * per_sm * waves);
+        return (int)(g < 1 ? 1 : min64(g, heads));
+    };
     if (a.P != nullptr) {
         e = launch_append_basis(E::kBytes == 4 ? kF32 : kBF16, a, s);
+    } else {
+        AppendArgs k = a;
+        k.group = heads_per_cta(runs, a.H_kv, E::kBytes == 2 ? 2 : 1, 3);
+        k.chunks = (a.H_kv + k.group - 1) / k.group;
+        if (runs * k.chunks > 0x7fffffff) return cudaErrorInvalidValue;
+        auto kern = k_append_keys<E, kQ8>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunRows * 128 * 4);
         if (e != cudaSuccess) return e;
-        behind = true;
+        const size_t smem = a.rope != nullptr ? (size_t)kRunRows * a.rot_dim * sizeof(float) : 0;
+        e = launch_kernel(kern, dim3((unsigned)(runs * k.chunks)), dim3(kStThreads), smem, s, false, k);
     }
-    // heads of a CTA: three CTAs for every place on the device, or one head
-    const int heads = (a.P == nullptr ? 2 : 1) * a.H_kv + (a.q != nullptr ? a.H_q : 0);
-    const int64_t runs = (((int64_t)a.T + kStRows - 2) / kStRows + 1) * a.B;
-    int64_t group = runs * heads / (di.sm_count * 6);
-    group = group < 1 ? 1 : min64(group, min64(heads, 16));
-    a.group = (int)group;
-    a.chunks = (int)((heads + group - 1) / group);
-    if (runs * a.chunks > 0x7fffffff) return cudaErrorInvalidValue;
-    auto kern = k_append_stream<E, kQ8>;
-    const size_t smem = a.rope != nullptr ? (size_t)kStRows * a.rot_dim * sizeof(float) : 0;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStRows * 128 * 4);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3((unsigned)(runs * a.chunks)), dim3(kStThreads), smem, s, behind, a);
+    const int per_sm = E::kBytes == 2 ? 3 : 2;
+    a.group = heads_per_cta(runs, a.H_kv, per_sm, 3);
+    a.chunks = (a.H_kv + a.group - 1) / a.group;
+    int64_t q_ctas = 0;
+    if (a.q != nullptr) {
+        const int64_t rows = ((int64_t)a.T + kStQueryRows - 1) / kStQueryRows * a.B;
+        a.q_group = heads_per_cta(rows, a.H_q, per_sm, 3);
+        a.q_group = (a.q_group + 3) & ~3;
+        a.q_chunks = (a.H_q + a.q_group - 1) / a.q_group;
+        q_ctas = rows * a.q_chunks;
+    }
+    if (runs * a.chunks + q_ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    a.kv_ctas = (int)(runs * a.chunks);
+    return launch_kernel(k_append_stream<E, kQ8>, dim3((unsigned)(a.kv_ctas + q_ctas)), dim3(kStThreads), 0, s, true, a);
 }
 
 cudaError_t launch_append_paged(Dt dt, AppendArgs a, cudaStream_t s) {

@@ -14,6 +14,7 @@
 
 #include "launch.h"
 #include "q8.cuh"
+#include "seqs.cuh"
 #include "tma.cuh"
 
 namespace loki {
@@ -41,6 +42,26 @@ __device__ __forceinline__ ApSeq append_seq(const AppendArgs& a, int b, bool fla
     if (a.rope != nullptr && a.n_pos < lim) lim = a.n_pos;
     s.hi = s.hi < lim ? s.hi : lim;
     return s;
+}
+
+// A row is worked on in aligned runs of 128 positions.
+constexpr int kRunRows = 128;
+
+// runs that positions [lo, hi) touch
+__device__ __forceinline__ int run_count(int64_t lo, int64_t hi) {
+    return hi > lo ? (int)((hi - 1) / kRunRows - lo / kRunRows) + 1 : 0;
+}
+
+// the largest finite magnitude of x[0 .. N) and amax
+template <int N>
+__device__ __forceinline__ float finite_amax(float amax, const float* x) {
+    float m = amax;
+#pragma unroll
+    for (int e = 0; e < N; ++e) m = fmaxf(m, fabsf(x[e]));  // (a NaN does not count)
+    if (m <= 3.402823466e38f) return m;
+#pragma unroll
+    for (int e = 0; e < N; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+    return amax;
 }
 
 // pool row of (sequence b, KV head hk, position j), or -1 (flagged) when its

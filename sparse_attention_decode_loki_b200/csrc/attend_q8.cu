@@ -56,6 +56,7 @@
 
 #include "launch.h"
 #include "q8.cuh"
+#include "seqs.cuh"
 #include "tma.cuh"
 
 namespace loki {
@@ -408,27 +409,11 @@ __device__ __forceinline__ int64_t q8_len(const AttendQ8Args& a, int b) {
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
-// tiles of the sequences before b (per KV head), and of all
-__device__ __forceinline__ void q8_tiles(const AttendQ8Args& a, int b, int64_t* before, int64_t* total) {
-    int64_t x = 0, y = 0;
-    for (int i = threadIdx.x & 31; i < a.B; i += 32) {
-        const int64_t n = (q8_len(a, i) + kTile - 1) / kTile;
-        y += n;
-        if (i < b) x += n;
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, off);
-        y += __shfl_xor_sync(0xffffffffu, y, off);
-    }
-    *before = x;
-    *total = y;
-}
-
-// a / b, b > 0: most lines of tiles are short enough for the 32-bit division
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
+// tiles of sequence b (per KV head)
+struct SeqTiles {
+    const AttendQ8Args& a;
+    __device__ __forceinline__ int64_t operator()(int b) const { return (q8_len(a, b) + kTile - 1) / kTile; }
+};
 
 // The line of `total` tiles in runs: a.warps / 2 of `per`, then a.warps / 2 of `tail`.
 struct Runs {
@@ -451,30 +436,6 @@ struct Runs {
         return tile < split ? quot(tile, per) : first + quot(tile - split, tail);
     }
 };
-
-// the sequence of tile w (counting H_kv runs of tiles per sequence)
-__device__ __forceinline__ int q8_find(const AttendQ8Args& a, int64_t w, int64_t* before) {
-    const int lane = threadIdx.x & 31;
-    int64_t carry = 0;
-    for (int base = 0; base < a.B; base += 32) {
-        int64_t n = base + lane < a.B ? (q8_len(a, base + lane) + kTile - 1) / kTile : 0;
-        const int64_t own = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, n, off);
-            if (lane >= off) n += o;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, w < a.H_kv * (carry + n));
-        if (hit != 0) {
-            const int at = __ffs(hit) - 1;
-            *before = carry + __shfl_sync(0xffffffffu, n - own, at);
-            return base + at;
-        }
-        carry += __shfl_sync(0xffffffffu, n, 31);
-    }
-    *before = 0;
-    return -1;
-}
 
 // partial `slot` of G heads in the workspace
 __device__ __forceinline__ float2* slot_ml(const AttendQ8Args& a, int64_t slot, int G) {
@@ -563,13 +524,13 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
         w = t = cw * per;
         w_end = min(t + per, n);
     } else {
-        int64_t before, total;
-        q8_tiles(a, 0, &before, &total);
-        const Runs runs(a, total * a.H_kv);  // (q8_find's lengths come from the L1)
+        int64_t before;
+        const SeqTiles tiles{a};
+        const Runs runs(a, seqs_total(a.B, tiles) * a.H_kv);  // (seqs_find's lengths come from the L1)
         w = runs.begin(wi);
         w_end = runs.end(wi);
         if (w >= w_end) return;
-        b = q8_find(a, w, &before);
+        b = seqs_find(a.B, w, a.H_kv, tiles, &before);
         if (b < 0) return;
         len = (int)q8_len(a, b);
         n = (len + kTile - 1) / kTile;
@@ -829,8 +790,7 @@ __global__ void __launch_bounds__(32 * W) k_q8_combine(const AttendQ8Args a) {
         Gc = a.H_q / a.H_kv;
         const int b = (int)(r / a.H_q), h = (int)(r % a.H_q);
         int64_t before;
-        q8_tiles(a, b, &before, &total);
-        total *= a.H_kv;
+        total = seqs_total(a.B, SeqTiles{a}, b, &before) * a.H_kv;
         n = (q8_len(a, b) + kTile - 1) / kTile;
         g = h % Gc;
         unit = (int64_t)b * a.H_kv + h / Gc;

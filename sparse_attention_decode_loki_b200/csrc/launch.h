@@ -196,7 +196,7 @@ struct AppendArgs {
     int64_t n_pages = 0;
     // set by the launchers
     int page_log2 = 0;  // -1: not a power of two
-    int block_log2 = 0, group = 0, chunks = 0, kv_ctas = 0;
+    int block_log2 = 0, group = 0, chunks = 0, q_group = 0, q_chunks = 1, kv_ctas = 0;
     int* err = nullptr;
 };
 cudaError_t launch_append_paged(Dt dt, AppendArgs a, cudaStream_t s);
