@@ -16,18 +16,22 @@
 //   D [128 x D] fp32 in tensor memory, read back one row to a lane.
 //
 // A persistent CTA takes consecutive tiles with the head slowest, so most keep
-// their P. The next tile's keys are loaded while the tensor cores and the
-// epilogue work. Rows that hold an infinity or a NaN take the plain fp32 sum
-// instead (an infinity has no second part).
+// their P. Its two groups of eight warps take the tiles in turn, each with an A
+// and an accumulator of its own: while one group's product runs (1.1 us) or its
+// loads are on their way, the other turns, splits, scales or stores. Stores go
+// through shared memory (a lane holds one row: stored directly, each 16 bytes
+// would touch another line, which took 1.5 us a tile). Rows that hold an
+// infinity or a NaN take the plain fp32 sum instead (an infinity has no second
+// part).
 #include <cuda_fp16.h>
 
 #include "append_paged.cuh"
 
 namespace loki {
 
-constexpr int kAbThreads = 256, kAbRows = 128;
-constexpr int kAbAtom = kAbRows * 128;  // bytes of 128 rows of 64 fp16 columns
-constexpr int kAbSmem = 8 * kAbAtom + 1024;
+constexpr int kAbGroup = 256, kAbThreads = 2 * kAbGroup;
+constexpr int kAbAtom = kRunRows * 128;  // bytes of 128 rows of 64 fp16 columns
+constexpr int kAbSmem = 12 * kAbAtom + 1024;
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, eight rows of
 // 128 bytes to a group, groups 1024 bytes apart.
@@ -80,271 +84,313 @@ __device__ __forceinline__ void put_parts(uint8_t* m, int row, int col, const fl
     *reinterpret_cast<uint4*>(at + 2 * kAbAtom) = lo;
 }
 
-// aligned runs of 128 positions that sequence b's written tokens touch
-__device__ __forceinline__ int append_runs(const ApSeq& s) {
-    return s.hi > s.lo ? (int)((s.hi - 1) / kAbRows - s.lo / kAbRows) + 1 : 0;
-}
+// byte `at` (a multiple of 16) of staged row r of `pitch` bytes: 16-byte chunks
+// swizzled, for lanes a row apart as well as for lanes along a row
+__device__ __forceinline__ int stage_at(int r, int at, int pitch) { return r * pitch + (at ^ ((r & 7) << 4)); }
+
+// what a group keeps beside its A
+struct GroupShared {
+    float row_down[kRunRows], red[2][kRunRows / 16];
+    int place[kRunRows];  // the tile's rows in the pool, -1: not written
+    int dead;             // a wait gave up
+    uint8_t odd_row[kRunRows];
+};
 
 template <class E, int D, bool kQ8>
 __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs a) {
     using Tp = typename E::T;
-    constexpr int DH = D / 2;  // an epilogue thread's columns
+    constexpr int DH = D / 2, DQ = D / 4;  // an epilogue thread's columns; a thread's rows of P
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float col_down[128];
-    __shared__ float row_down[kAbRows], red[2][kAbRows / 16];
-    __shared__ uint8_t odd_row[kAbRows];
-    __shared__ __align__(8) uint64_t bar;
+    __shared__ float col_top[4][128];
+    __shared__ GroupShared group_shared[2];
+    __shared__ __align__(8) uint64_t bars[2];
     __shared__ uint32_t tmem_slot;
-    uint8_t* A = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
-    uint8_t* Bm = A + 4 * kAbAtom;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 8, gt = tid & 255, warp = gt >> 5;
+    uint8_t* Bm = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    uint8_t* A = Bm + (1 + grp) * 4 * kAbAtom;
+    GroupShared& sh = group_shared[grp];
+    uint64_t* bar = bars + grp;
+    auto group_sync = [&]() { named_sync(1 + grp, kAbGroup); };
     griddep_launch_dependents();
 
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tmem_slot))
+    if (tid < 32) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (tid == 0) {
-        mbar_init(&bar, 1);
+    if (gt == 0) {
+        mbar_init(bar, 1);
         fence_mbar_init();
+        sh.dead = 0;
     }
     // this CTA's tiles: heads slowest, then sequences, then their runs
-    int64_t R = 0;
-    for (int i = lane; i < a.B; i += 32) R += append_runs(append_seq(a, i, false));
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) R += __shfl_xor_sync(0xffffffffu, R, off);
-    const int64_t total = R * a.H_kv, per = (total + gridDim.x - 1) / gridDim.x;
-    int64_t w = blockIdx.x * per;
+    auto runs_of = [&](int b) -> int64_t {
+        const ApSeq s = append_seq(a, b, false);
+        return run_count(s.lo, s.hi);
+    };
+    const int64_t R = seqs_total(a.B, runs_of), total = R * a.H_kv, per = quot(total + gridDim.x - 1, gridDim.x);
+    int64_t w = min64(blockIdx.x * per, total);
     const int64_t w_end = min64(w + per, total);
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = tmem_slot + grp * 128;
+    constexpr uint32_t idesc = 1u << 4 | (uint32_t)(D >> 3) << 17 | (uint32_t)(kRunRows >> 4) << 24;
 
-    int hk = -1, b = 0, run = 0, runs = 0;
+    // the tile at hand or next: run `run` of sequence b under head hk
+    int hk = 0, b = 0, run = 0, runs = 0;
     ApSeq sq{};
-    if (w < w_end) {
-        hk = (int)(w / R);
-        int64_t skip = w % R;
-        for (;; ++b) {  // total > w: some sequence holds it
+    auto seek = [&](int step) {
+        run += step;
+        while (run >= runs) {
+            run -= runs;
+            ++b;
             sq = append_seq(a, b, false);
-            runs = append_runs(sq);
-            if (skip < runs) break;
-            skip -= runs;
+            runs = run_count(sq.lo, sq.hi);
         }
-        run = (int)skip;
-    }
-
-    // keys of a tile as loaded: four rows a thread, unit u of each
+    };
+    // its rows as loaded, four a thread, unit u of each, and the first row's angles
     const int u = lane & 7, sub = lane >> 3;
     const bool unit_on = u < D / 16, turn = a.rope != nullptr && u < a.rot_dim >> 4;
     int ca, cb;
     unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
     Chunk<E> wa[4], wb[4];
-    bool live[4];
+    Angles g;
+    uint32_t live = 0;
     auto load = [&]() {
-        const int64_t start = (sq.lo / kAbRows + run) * kAbRows;
-        const Tp* rows = static_cast<const Tp*>(a.K_new) + ((int64_t)b * a.H_kv + hk) * a.T * D;
+        const int64_t j0 = (sq.lo / kRunRows + run) * kRunRows + 16 * warp + sub;
+        const Tp* p = static_cast<const Tp*>(a.K_new) + (((int64_t)b * a.H_kv + hk) * a.T + (j0 - sq.p0)) * D;
+        live = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t j = start + 16 * warp + 4 * i + sub;
-            live[i] = unit_on && j >= sq.lo && j < sq.hi;
-            if (live[i]) {
-                wa[i].load(rows + (j - sq.p0) * D + ca);
-                wb[i].load(rows + (j - sq.p0) * D + cb);
+        for (int i = 0; i < 4; ++i)
+            if (unit_on && j0 + 4 * i >= sq.lo && j0 + 4 * i < sq.hi) {
+                live |= 1u << i;
+                wa[i].load(p + 4 * i * D + ca);
+                wb[i].load(p + 4 * i * D + cb);
             }
-        }
+        if (turn && (live & 1u)) g.load(a.rope + j0 * a.rot_dim, a.rot_dim, u);
     };
-    if (w < w_end) load();
 
-    const uint32_t idesc = 1u << 4 | (uint32_t)(D >> 3) << 17 | (uint32_t)(kAbRows >> 4) << 24;
-    int held = -1;  // the head whose P is in shared memory
     uint32_t phase = 0;
-    while (w < w_end) {
-        const int64_t start = (sq.lo / kAbRows + run) * kAbRows, lo = sq.lo, hi = sq.hi, p0 = sq.p0;
-        const int tb = b, th = hk;
-        if (held != th) {
-            held = th;
-            const float* Ph = a.P + (int64_t)th * D * D;
-            // two threads to a column: its rows' largest magnitude, then its parts
-            const int c = tid & 127, half = tid >> 7;
-            float x[8], top = 0.f;
-            if (c < D)
-                for (int i = 0; i < D; ++i) top = fmaxf(top, finite_abs(__ldg(Ph + i * D + c)));
-            const int e = lift(top);
-            const float up = pow2(e);
-            if (half == 0) col_down[c] = pow2(-e);
-            if (c < D)
-                for (int i = half * DH; i < half * DH + DH; i += 8) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = __ldg(Ph + (i + k) * D + c);
-                    put_parts(Bm, c, i, x, up);
-                }
-        }
-        // rotation, then the rows' parts
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 16 * warp + 4 * i + sub;
-            float x[16], top = 0.f;
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;
-            if (live[i]) {
-                wa[i].get(x);
-                wb[i].get(x + 8);
-                if (turn) turn_unit(a.rope, a.rot_dim, a.interleaved, start + r, u, x);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float m = fabsf(x[e]);
-                odd |= !(m <= 3.402823466e38f);
-                top = fmaxf(top, m);
-            }
-#pragma unroll
-            for (int off = 1; off <= 4; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            odd = (__ballot_sync(0xffffffffu, odd) >> (lane & 24) & 0xffu) != 0;
-            const int e = odd ? 0 : lift(top);
-            if (u == 0) {
-                row_down[r] = pow2(-e);
-                odd_row[r] = odd;
-            }
-            if (unit_on) {
-                put_parts(A, r, ca, x, pow2(e));
-                put_parts(A, r, cb, x + 8, pow2(e));
-            }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncthreads();
-        if (tid == 0) {
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t sa = smem_addr(A), sb = smem_addr(Bm);
-#pragma unroll
-            for (int pass = 0; pass < 3; ++pass)
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = (k >> 2) * kAbAtom + (k & 3) * 32;
-                    mma_f16_ss(tmem, smem_desc(sa + (pass == 2 ? 2 * kAbAtom : 0) + at),
-                               smem_desc(sb + (pass == 1 ? 2 * kAbAtom : 0) + at), idesc, pass + k > 0);
-                }
-            asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                             smem_addr(&bar))
-                         : "memory");
-        }
-        // the next tile's keys, meanwhile
-        if (++w < w_end) {
-            if (++run == runs) {
-                run = 0;
-                do {
-                    if (++b == a.B) {
-                        b = 0;
-                        ++hk;
-                    }
-                    sq = append_seq(a, b, false);
-                    runs = append_runs(sq);
-                } while (runs == 0);
-            }
+    bool alive = true;
+    int64_t ri = 0;  // w's place under its head
+    if (w < w_end) {
+        hk = (int)quot(w, R);
+        ri = w - hk * R;
+    }
+    for (; w < w_end; ++hk, ri = 0) {  // head by head
+        int64_t left = min64(w_end - w, R - ri);  // tiles under this head, the groups' in turn
+        w += left;
+        left -= grp;
+        if (left > 0) {
+            int64_t before;
+            b = seqs_find(a.B, ri, 1, runs_of, &before);
+            sq = append_seq(a, b, false);
+            runs = run_count(sq.lo, sq.hi);
+            run = (int)(ri - before);
+            seek(grp);
             load();
         }
-        // this thread's row of the product, half of its columns
-        const int r = (warp & 3) * 32 + lane, half = warp >> 2;
-        const int64_t j = start + r;
-        const bool mine = j >= lo && j < hi;
-        const bool has_row = mine || (kQ8 && j < lo);
-        const int block_start = kQ8 ? (int)(j & ~(int64_t)(a.block - 1)) : 0;
-        // older rows of a block that receives tokens count too: they may move to a larger scale
-        const bool has_new = kQ8 && block_start < hi && block_start + a.block > lo;
-        const bool has_old = kQ8 && lo > block_start;
-        int row = -1;
-        float old = 0.f;
-        if (kQ8 ? (has_row && has_new) : mine) row = pool_row(a, tb, th, (int)j);
-        if (kQ8 && row >= 0 && has_old) old = a.k_scales[row >> a.block_log2];
-        const bool done = mbar_wait(&bar, phase, a.err);
-        phase ^= 1;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        float y[DH];
+        __syncthreads();  // no product reads the last head's P any more
+        {
+            // four threads to a column, a quarter of its rows each: the largest magnitude, then the parts
+            const int c = tid & 127, i0 = (tid >> 7) * DQ;
+            float x[DQ], top = 0.f;
+            if (c < D) {
+                const float* Ph = a.P + (int64_t)hk * D * D + i0 * D + c;
 #pragma unroll
-        for (int i = 0; i < DH; i += 16) tmem_ld16(y + i, tmem + ((uint32_t)(warp & 3) << 21) + half * DH + i);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        const float down = row_down[r];
-#pragma unroll
-        for (int i = 0; i < DH; i += 4) {
-            const float4 cd = *reinterpret_cast<const float4*>(&col_down[half * DH + i]);
-            y[i] = y[i] * down * cd.x;
-            y[i + 1] = y[i + 1] * down * cd.y;
-            y[i + 2] = y[i + 2] * down * cd.z;
-            y[i + 3] = y[i + 3] * down * cd.w;
-        }
-        if (mine && odd_row[r]) {
-#pragma unroll
-            for (int i = 0; i < DH; ++i) y[i] = 0.f;
-            const Tp* K = static_cast<const Tp*>(a.K_new) + (((int64_t)tb * a.H_kv + th) * a.T + (j - p0)) * D;
-            const float* Ph = a.P + (int64_t)th * D * D + half * DH;
-            for (int i = 0; i < D; ++i) {
-                const float x = turned_col<E>(a, K, j, i);
-#pragma unroll
-                for (int c = 0; c < DH; ++c) y[c] = fmaf(x, __ldg(Ph + i * D + c), y[c]);
+                for (int i = 0; i < DQ; ++i) x[i] = __ldg(Ph + i * D);
+                top = finite_amax<DQ>(0.f, x);
             }
-        }
-        if (mine && row >= 0 && a.plane != nullptr) {
-            Tp* o = static_cast<Tp*>(a.plane) + (int64_t)row * a.d_lo + half * DH;
+            col_top[tid >> 7][c] = top;
+            __syncthreads();
+            const int e = lift(fmaxf(fmaxf(col_top[0][c], col_top[1][c]), fmaxf(col_top[2][c], col_top[3][c])));
+            if (tid < 128) col_down[c] = pow2(-e);
+            if (c < D) {
 #pragma unroll
-            for (int i = 0; i < DH; i += E::kVec)
-                if (half * DH + i < a.d_lo) *reinterpret_cast<uint4*>(o + i) = pack16(y + i, E());
-        }
-        if constexpr (!kQ8) {
-            if (mine && row >= 0) {
-                Tp* o = static_cast<Tp*>(a.K_pages) + (int64_t)row * D + half * DH;
-#pragma unroll
-                for (int i = 0; i < DH; i += E::kVec) *reinterpret_cast<uint4*>(o + i) = pack16(y + i, E());
+                for (int i = 0; i < DQ; i += 8) put_parts(Bm, c, i0 + i, x + i, pow2(e));
             }
-        } else {
-            float top = 0.f;
-            if (mine) {
-#pragma unroll
-                for (int i = 0; i < DH; ++i) top = fmaxf(top, finite_abs(y[i]));
-            }
-#pragma unroll
-            for (int off = 1; off <= 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            if ((lane & 15) == 0) red[half][r >> 4] = top;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        // the tile's reads of tensor and shared memory are over (8 bits: its
-        // magnitudes are there, and every row has read its block's old scale)
-        if (__syncthreads_or(!done)) break;
-        if constexpr (kQ8) {
-            if (row >= 0) {
-                const int g0 = (r & ~(a.block - 1)) >> 4;
-                float top = 0.f;
-                for (int g = g0; g < g0 + (a.block >> 4); ++g) top = fmaxf(top, fmaxf(red[0][g], red[1][g]));
-                const float grown = pow2_scale(top), s = has_old ? fmaxf(old, grown) : grown;
-                uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.K_pages) + (int64_t)row * D + half * DH);
-                if (mine) {
-                    const float inv = 1.f / s;
+        for (; alive && left > 0; left -= 2) {
+            const int64_t start = (sq.lo / kRunRows + run) * kRunRows, lo = sq.lo, hi = sq.hi, p0 = sq.p0;
+            const int tb = b;
+            // rotation, then the rows' parts; the next row's angles on their way
 #pragma unroll
-                    for (int i = 0; i < DH; i += 16) {
-                        const uint2 p = codes8(y + i, inv), q = codes8(y + i + 8, inv);
-                        o[i >> 4] = make_uint4(p.x, p.y, q.x, q.y);
-                    }
-                    if (half == 0 && j == (block_start > lo ? block_start : lo)) a.k_scales[row >> a.block_log2] = s;
-                } else if (s > old) {
-                    const float f = old / s;
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * warp + 4 * i + sub;
+                Angles next;
+                if (i < 3 && turn && (live >> (i + 1) & 1u))
+                    next.load(a.rope + (start + r + 4) * a.rot_dim, a.rot_dim, u);
+                float x[16], top = 0.f, zero = 0.f;  // zero: 0, or NaN where an entry is infinite or NaN
 #pragma unroll
-                    for (int i = 0; i < DH >> 4; ++i) {
-                        uint4 v = o[i];
-                        v.x = rescale4(v.x, f);
-                        v.y = rescale4(v.y, f);
-                        v.z = rescale4(v.z, f);
-                        v.w = rescale4(v.w, f);
-                        o[i] = v;
-                    }
+                for (int e = 0; e < 16; ++e) x[e] = 0.f;
+                if (live >> i & 1u) {
+                    wa[i].get(x);
+                    wb[i].get(x + 8);
+                    if (turn) g.turn(x, a.interleaved);
                 }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    top = fmaxf(top, fabsf(x[e]));
+                    zero = fmaf(x[e], 0.f, zero);
+                }
+#pragma unroll
+                for (int off = 1; off <= 4; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const bool odd = (__ballot_sync(0xffffffffu, zero != 0.f) >> (lane & 24) & 0xffu) != 0;
+                const int e = odd ? 0 : lift(top);
+                if (u == 0) {
+                    sh.row_down[r] = pow2(-e);
+                    sh.odd_row[r] = odd;
+                }
+                if (unit_on) {
+                    put_parts(A, r, ca, x, pow2(e));
+                    put_parts(A, r, cb, x + 8, pow2(e));
+                }
+                if (i < 3) g = next;
             }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            group_sync();
+            if (gt == 0) {
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t sa = smem_addr(A), sb = smem_addr(Bm);
+#pragma unroll 1
+                for (int pass = 0; pass < 3; ++pass)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k >> 2) * kAbAtom + (k & 3) * 32;
+                        mma_f16_ss(tmem, smem_desc(sa + (pass == 2 ? 2 * kAbAtom : 0) + at),
+                                   smem_desc(sb + (pass == 1 ? 2 * kAbAtom : 0) + at), idesc, pass + k > 0);
+                    }
+                asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_addr(bar))
+                             : "memory");
+            }
+            __syncwarp();
+            if (left > 2) {  // the group's next tile, meanwhile
+                seek(2);
+                load();
+            }
+            // this thread's row of the product, half of its columns
+            const int r = (warp & 3) * 32 + lane, c0 = (warp >> 2) * DH;
+            const int64_t j = start + r;
+            const bool mine = j >= lo && j < hi;
+            const int block_start = kQ8 ? (int)(j & ~(int64_t)(a.block - 1)) : 0;
+            // older rows of a block that receives tokens count too: they may move to a larger scale
+            const bool has_new = kQ8 && j < hi && block_start + a.block > lo;
+            const bool has_old = kQ8 && lo > block_start;
+            int row = -1;
+            float old = 0.f;
+            if (kQ8 ? has_new : mine) row = pool_row(a, tb, hk, (int)j);
+            if (kQ8 && row >= 0 && has_old) old = a.k_scales[row >> a.block_log2];
+            const bool write = mine && row >= 0;
+            if (!mbar_wait(bar, phase, a.err)) sh.dead = 1;
+            phase ^= 1;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t cols = tmem + ((uint32_t)(warp & 3) << 21);
+            const float down = sh.row_down[r];
+            const bool odd = mine && sh.odd_row[r];
+            // columns c .. c + 15 of the row, times f / down
+            auto columns = [&](int c, float* y, float f) {
+                tmem_ld16(y, cols + c);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 cd = *reinterpret_cast<const float4*>(&col_down[c + i]);
+                    y[i] = y[i] * cd.x * f;
+                    y[i + 1] = y[i + 1] * cd.y * f;
+                    y[i + 2] = y[i + 2] * cd.z * f;
+                    y[i + 3] = y[i + 3] * cd.w * f;
+                }
+                if (!odd) return;
+                const Tp* K = static_cast<const Tp*>(a.K_new) + (((int64_t)tb * a.H_kv + hk) * a.T + (j - p0)) * D;
+                const float* Ph = a.P + (int64_t)hk * D * D + c;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < D; ++i) {
+                    const float x = turned_col<E>(a, K, j, i);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] = fmaf(x, __ldg(Ph + i * D + e), y[e]);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] *= f;  // (an odd row's down is 1)
+            };
+            // The tile's outputs go into A, whose product is done: rows of the cache's type (8 bits: of the
+            // plane, as far as they fit in front of the codes).
+            uint8_t* stage8 = A + 3 * kAbAtom;
+            const int lo_bytes = a.plane != nullptr ? a.d_lo * E::kBytes : 0;
+            const int pitch = kQ8 ? (lo_bytes + 127) & ~127 : 128 * E::kBytes;  // whole swizzles
+            const bool staged = !kQ8 || pitch * kRunRows <= 3 * kAbAtom;
+            float top = 0.f;
+#pragma unroll
+            for (int c = c0; c < c0 + DH; c += 16) {
+                float y[16];
+                columns(c, y, down);
+                if (!kQ8 || (c < a.d_lo && staged)) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += E::kVec)
+                        if (!kQ8 || c + i < a.d_lo)
+                            *reinterpret_cast<uint4*>(A + stage_at(r, (c + i) * E::kBytes, pitch)) = pack16(y + i, E());
+                } else if (write && c < a.d_lo) {
+                    Tp* o = static_cast<Tp*>(a.plane) + (int64_t)row * a.d_lo + c;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 8) store_chunk<E>(o + i, y + i, c + i, a.d_lo);
+                }
+                if (kQ8 && mine) top = finite_amax<16>(top, y);
+            }
+            if constexpr (kQ8) {
+#pragma unroll
+                for (int off = 1; off <= 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                if ((lane & 15) == 0) sh.red[warp >> 2][r >> 4] = top;
+            }
+            if (c0 == 0) sh.place[r] = write ? row : -1;
+            group_sync();  // staged (8 bits: magnitudes are there, and every row has read its block's old scale)
+            alive = sh.dead == 0;
+            if (!alive) break;
+            if constexpr (kQ8) {
+                const int g0 = (r & ~(a.block - 1)) >> 4;
+                top = 0.f;
+                for (int q = g0; q < g0 + (a.block >> 4); ++q) top = fmaxf(top, fmaxf(sh.red[0][q], sh.red[1][q]));
+                const float grown = pow2_scale(top), s = has_old ? fmaxf(old, grown) : grown;
+                const float f = fminf(down * (1.f / s), 3.402823466e38f);
+#pragma unroll
+                for (int c = c0; c < c0 + DH; c += 16) {
+                    float y[16];
+                    columns(c, y, f);
+                    const uint2 p = codes8(y, 1.f), q = codes8(y + 8, 1.f);
+                    *reinterpret_cast<uint4*>(stage8 + stage_at(r, c, 128)) = make_uint4(p.x, p.y, q.x, q.y);
+                }
+                if (!write && row >= 0 && has_old && s > old) {
+                    uint32_t* v = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.K_pages) + (int64_t)row * D + c0);
+                    for (int c = 0; c < DH / 4; ++c) v[c] = rescale4(v[c], old / s);
+                }
+                if (write && c0 == 0 && j == (block_start > lo ? block_start : lo)) a.k_scales[row >> a.block_log2] = s;
+                group_sync();
+            }
+            // the staged rows, 16 bytes a lane along the rows
+            auto copy_out = [&](const uint8_t* from, int from_pitch, void* pool, int bytes) {
+                const int per_row = bytes >> 4;
+                for (int i = gt; i < kRunRows * per_row; i += kAbGroup) {
+                    const int q = i / per_row, c = i - q * per_row, to = sh.place[q];
+                    if (to >= 0)
+                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + (int64_t)to * bytes + c * 16) =
+                            *reinterpret_cast<const uint4*>(from + stage_at(q, c * 16, from_pitch));
+                }
+            };
+            if constexpr (kQ8) copy_out(stage8, 128, a.K_pages, D);
+            else copy_out(A, 128 * E::kBytes, a.K_pages, D * E::kBytes);
+            if (lo_bytes > 0 && staged) copy_out(A, pitch, a.plane, lo_bytes);
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            group_sync();  // A and place may be written again
         }
     }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem));
+    if (tid < 32) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem_slot));
 }
 
 template <class E, bool kQ8>
@@ -355,7 +401,7 @@ static cudaError_t basis_impl(const AppendArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (((int64_t)a.T + kAbRows - 2) / kAbRows + 1) * a.B * a.H_kv;
+    const int64_t tiles = (((int64_t)a.T + kRunRows - 2) / kRunRows + 1) * a.B * a.H_kv;
     return launch_kernel(kern, dim3((unsigned)min64(tiles, di.sm_count)), dim3(kAbThreads), kAbSmem, s, false, a);
 }
 
