@@ -15,23 +15,22 @@
 //   both in shared memory, K-major, 128-byte swizzle, 64 columns to an atom;
 //   D [128 x D] fp32 in tensor memory, read back one row to a lane.
 //
-// A persistent CTA takes consecutive tiles with the head slowest, so most keep
-// their P. Its two groups of eight warps take the tiles in turn, each with an A
-// and an accumulator of its own: while one group's product runs (1.1 us) or its
-// loads are on their way, the other turns, splits, scales or stores. Stores go
-// through shared memory (a lane holds one row: stored directly, each 16 bytes
-// would touch another line, which took 1.5 us a tile). Rows that hold an
-// infinity or a NaN take the plain fp32 sum instead (an infinity has no second
-// part).
+// A persistent CTA of eight warps takes consecutive tiles with the head slowest,
+// so most keep their P. It leaves half of the SM's registers to the stream of
+// values and queries, which runs beside it as a programmatic dependent: both
+// wait on latencies most of the time. Stores go through shared memory (a lane
+// holds one row: stored directly, each 16 bytes would touch another line, which
+// took 1.5 us a tile). Rows that hold an infinity or a NaN take the plain fp32
+// sum instead (an infinity has no second part).
 #include <cuda_fp16.h>
 
 #include "append_paged.cuh"
 
 namespace loki {
 
-constexpr int kAbGroup = 256, kAbThreads = 2 * kAbGroup;
+constexpr int kAbThreads = 256;
 constexpr int kAbAtom = kRunRows * 128;  // bytes of 128 rows of 64 fp16 columns
-constexpr int kAbSmem = 12 * kAbAtom + 1024;
+constexpr int kAbSmem = 8 * kAbAtom + 1024;  // and the tile's angles behind them
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, eight rows of
 // 128 bytes to a group, groups 1024 bytes apart.
@@ -88,41 +87,33 @@ __device__ __forceinline__ void put_parts(uint8_t* m, int row, int col, const fl
 // swizzled, for lanes a row apart as well as for lanes along a row
 __device__ __forceinline__ int stage_at(int r, int at, int pitch) { return r * pitch + (at ^ ((r & 7) << 4)); }
 
-// what a group keeps beside its A
-struct GroupShared {
-    float row_down[kRunRows], red[2][kRunRows / 16];
-    int place[kRunRows];  // the tile's rows in the pool, -1: not written
-    int dead;             // a wait gave up
-    uint8_t odd_row[kRunRows];
-};
-
 template <class E, int D, bool kQ8>
-__global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs a) {
+__global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_basis(const AppendArgs a) {
     using Tp = typename E::T;
-    constexpr int DH = D / 2, DQ = D / 4;  // an epilogue thread's columns; a thread's rows of P
+    constexpr int DH = D / 2;  // an epilogue thread's columns, and a thread's rows of P
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float col_down[128];
-    __shared__ float col_top[4][128];
-    __shared__ GroupShared group_shared[2];
-    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ float col_top[2][128];
+    __shared__ float row_down[kRunRows], red[2][kRunRows / 16];
+    __shared__ int place[kRunRows];  // the tile's rows in the pool, -1: not written
+    __shared__ uint8_t odd_row[kRunRows];
+    __shared__ __align__(8) uint64_t bar, angle_bar;
     __shared__ uint32_t tmem_slot;
-    const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 8, gt = tid & 255, warp = gt >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* Bm = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
-    uint8_t* A = Bm + (1 + grp) * 4 * kAbAtom;
-    GroupShared& sh = group_shared[grp];
-    uint64_t* bar = bars + grp;
-    auto group_sync = [&]() { named_sync(1 + grp, kAbGroup); };
+    uint8_t* A = Bm + 4 * kAbAtom;
+    float* angles = reinterpret_cast<float*>(A + 4 * kAbAtom);  // [128][rot_dim]
     griddep_launch_dependents();
 
-    if (tid < 32) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_addr(&tmem_slot))
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (gt == 0) {
-        mbar_init(bar, 1);
+    if (tid == 0) {
+        mbar_init(&bar, 1);
+        mbar_init(&angle_bar, 1);
         fence_mbar_init();
-        sh.dead = 0;
     }
     // this CTA's tiles: heads slowest, then sequences, then their runs
     auto runs_of = [&](int b) -> int64_t {
@@ -135,32 +126,27 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const uint32_t tmem = tmem_slot + grp * 128;
+    const uint32_t tmem = tmem_slot;
     constexpr uint32_t idesc = 1u << 4 | (uint32_t)(D >> 3) << 17 | (uint32_t)(kRunRows >> 4) << 24;
 
     // the tile at hand or next: run `run` of sequence b under head hk
     int hk = 0, b = 0, run = 0, runs = 0;
     ApSeq sq{};
-    auto seek = [&](int step) {
-        run += step;
-        while (run >= runs) {
-            run -= runs;
-            ++b;
-            sq = append_seq(a, b, false);
-            runs = run_count(sq.lo, sq.hi);
-        }
-    };
-    // its rows as loaded, four a thread, unit u of each, and the first row's angles
-    const int u = lane & 7, sub = lane >> 3;
-    const bool unit_on = u < D / 16, turn = a.rope != nullptr && u < a.rot_dim >> 4;
+    // its rows as loaded, four a thread, unit u of each, and its angles
+    const int u = lane & 7, sub = lane >> 3, rot = a.rope != nullptr ? a.rot_dim : 0;
+    const bool unit_on = u < D / 16, turn = u < rot >> 4;
     int ca, cb;
-    unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
+    unit_cols(turn ? rot : 0, a.interleaved, u, &ca, &cb);
     Chunk<E> wa[4], wb[4];
-    Angles g;
     uint32_t live = 0;
     auto load = [&]() {
-        const int64_t j0 = (sq.lo / kRunRows + run) * kRunRows + 16 * warp + sub;
+        const int64_t start = (sq.lo / kRunRows + run) * kRunRows, j0 = start + 16 * warp + sub;
         const Tp* p = static_cast<const Tp*>(a.K_new) + (((int64_t)b * a.H_kv + hk) * a.T + (j0 - sq.p0)) * D;
+        if (rot > 0 && tid == 0) {  // every reader of the angles before has passed a barrier
+            const uint32_t bytes = (uint32_t)min64(sq.hi - start, kRunRows) * rot * 4;
+            mbar_arrive_expect_tx(&angle_bar, bytes);
+            bulk_load(angles, a.rope + start * rot, bytes, &angle_bar);
+        }
         live = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -169,7 +155,6 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
                 wa[i].load(p + 4 * i * D + ca);
                 wb[i].load(p + 4 * i * D + cb);
             }
-        if (turn && (live & 1u)) g.load(a.rope + j0 * a.rot_dim, a.rot_dim, u);
     };
 
     uint32_t phase = 0;
@@ -180,57 +165,53 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
         ri = w - hk * R;
     }
     for (; w < w_end; ++hk, ri = 0) {  // head by head
-        int64_t left = min64(w_end - w, R - ri);  // tiles under this head, the groups' in turn
+        int64_t left = min64(w_end - w, R - ri);  // tiles under this head
         w += left;
-        left -= grp;
-        if (left > 0) {
+        {
             int64_t before;
             b = seqs_find(a.B, ri, 1, runs_of, &before);
             sq = append_seq(a, b, false);
             runs = run_count(sq.lo, sq.hi);
             run = (int)(ri - before);
-            seek(grp);
             load();
         }
         __syncthreads();  // no product reads the last head's P any more
         {
-            // four threads to a column, a quarter of its rows each: the largest magnitude, then the parts
-            const int c = tid & 127, i0 = (tid >> 7) * DQ;
-            float x[DQ], top = 0.f;
+            // two threads to a column, half of its rows each: the largest magnitude, then the parts
+            const int c = tid & 127, i0 = (tid >> 7) * DH;
+            float x[DH], top = 0.f;
             if (c < D) {
                 const float* Ph = a.P + (int64_t)hk * D * D + i0 * D + c;
 #pragma unroll
-                for (int i = 0; i < DQ; ++i) x[i] = __ldg(Ph + i * D);
-                top = finite_amax<DQ>(0.f, x);
+                for (int i = 0; i < DH; ++i) x[i] = __ldg(Ph + i * D);
+                top = finite_amax<DH>(0.f, x);
             }
             col_top[tid >> 7][c] = top;
             __syncthreads();
-            const int e = lift(fmaxf(fmaxf(col_top[0][c], col_top[1][c]), fmaxf(col_top[2][c], col_top[3][c])));
+            const int e = lift(fmaxf(col_top[0][c], col_top[1][c]));
             if (tid < 128) col_down[c] = pow2(-e);
             if (c < D) {
 #pragma unroll
-                for (int i = 0; i < DQ; i += 8) put_parts(Bm, c, i0 + i, x + i, pow2(e));
+                for (int i = 0; i < DH; i += 8) put_parts(Bm, c, i0 + i, x + i, pow2(e));
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
         }
-        for (; alive && left > 0; left -= 2) {
+        for (; alive && left > 0; --left) {
             const int64_t start = (sq.lo / kRunRows + run) * kRunRows, lo = sq.lo, hi = sq.hi, p0 = sq.p0;
             const int tb = b;
-            // rotation, then the rows' parts; the next row's angles on their way
+            // rotation, then the rows' parts
+            bool done = rot == 0 || mbar_wait(&angle_bar, phase, a.err);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 16 * warp + 4 * i + sub;
-                Angles next;
-                if (i < 3 && turn && (live >> (i + 1) & 1u))
-                    next.load(a.rope + (start + r + 4) * a.rot_dim, a.rot_dim, u);
                 float x[16], top = 0.f, zero = 0.f;  // zero: 0, or NaN where an entry is infinite or NaN
 #pragma unroll
                 for (int e = 0; e < 16; ++e) x[e] = 0.f;
                 if (live >> i & 1u) {
                     wa[i].get(x);
                     wb[i].get(x + 8);
-                    if (turn) g.turn(x, a.interleaved);
+                    if (turn) turn_unit_from(angles + r * rot, rot, a.interleaved, u, x);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -242,19 +223,18 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
                 const bool odd = (__ballot_sync(0xffffffffu, zero != 0.f) >> (lane & 24) & 0xffu) != 0;
                 const int e = odd ? 0 : lift(top);
                 if (u == 0) {
-                    sh.row_down[r] = pow2(-e);
-                    sh.odd_row[r] = odd;
+                    row_down[r] = pow2(-e);
+                    odd_row[r] = odd;
                 }
                 if (unit_on) {
                     put_parts(A, r, ca, x, pow2(e));
                     put_parts(A, r, cb, x + 8, pow2(e));
                 }
-                if (i < 3) g = next;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            group_sync();
-            if (gt == 0) {
+            __syncthreads();
+            if (tid == 0) {
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t sa = smem_addr(A), sb = smem_addr(Bm);
 #pragma unroll 1
@@ -266,12 +246,18 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
                                    smem_desc(sb + (pass == 1 ? 2 * kAbAtom : 0) + at), idesc, pass + k > 0);
                     }
                 asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                 smem_addr(bar))
+                                 smem_addr(&bar))
                              : "memory");
             }
             __syncwarp();
-            if (left > 2) {  // the group's next tile, meanwhile
-                seek(2);
+            if (left > 1) {  // the next tile, meanwhile
+                ++run;
+                while (run >= runs) {
+                    run = 0;
+                    ++b;
+                    sq = append_seq(a, b, false);
+                    runs = run_count(sq.lo, sq.hi);
+                }
                 load();
             }
             // this thread's row of the product, half of its columns
@@ -287,12 +273,12 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
             if (kQ8 ? has_new : mine) row = pool_row(a, tb, hk, (int)j);
             if (kQ8 && row >= 0 && has_old) old = a.k_scales[row >> a.block_log2];
             const bool write = mine && row >= 0;
-            if (!mbar_wait(bar, phase, a.err)) sh.dead = 1;
+            done = mbar_wait(&bar, phase, a.err) && done;
             phase ^= 1;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t cols = tmem + ((uint32_t)(warp & 3) << 21);
-            const float down = sh.row_down[r];
-            const bool odd = mine && sh.odd_row[r];
+            const float down = row_down[r];
+            const bool odd = mine && odd_row[r];
             // columns c .. c + 15 of the row, times f / down
             auto columns = [&](int c, float* y, float f) {
                 tmem_ld16(y, cols + c);
@@ -345,16 +331,16 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
             if constexpr (kQ8) {
 #pragma unroll
                 for (int off = 1; off <= 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                if ((lane & 15) == 0) sh.red[warp >> 2][r >> 4] = top;
+                if ((lane & 15) == 0) red[warp >> 2][r >> 4] = top;
             }
-            if (c0 == 0) sh.place[r] = write ? row : -1;
-            group_sync();  // staged (8 bits: magnitudes are there, and every row has read its block's old scale)
-            alive = sh.dead == 0;
+            if (c0 == 0) place[r] = write ? row : -1;
+            // staged (8 bits: magnitudes are there, and every row has read its block's old scale)
+            alive = !__syncthreads_or(!done);
             if (!alive) break;
             if constexpr (kQ8) {
                 const int g0 = (r & ~(a.block - 1)) >> 4;
                 top = 0.f;
-                for (int q = g0; q < g0 + (a.block >> 4); ++q) top = fmaxf(top, fmaxf(sh.red[0][q], sh.red[1][q]));
+                for (int q = g0; q < g0 + (a.block >> 4); ++q) top = fmaxf(top, fmaxf(red[0][q], red[1][q]));
                 const float grown = pow2_scale(top), s = has_old ? fmaxf(old, grown) : grown;
                 const float f = fminf(down * (1.f / s), 3.402823466e38f);
 #pragma unroll
@@ -369,13 +355,20 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
                     for (int c = 0; c < DH / 4; ++c) v[c] = rescale4(v[c], old / s);
                 }
                 if (write && c0 == 0 && j == (block_start > lo ? block_start : lo)) a.k_scales[row >> a.block_log2] = s;
-                group_sync();
+                __syncthreads();
             }
             // the staged rows, 16 bytes a lane along the rows
             auto copy_out = [&](const uint8_t* from, int from_pitch, void* pool, int bytes) {
                 const int per_row = bytes >> 4;
-                for (int i = gt; i < kRunRows * per_row; i += kAbGroup) {
-                    const int q = i / per_row, c = i - q * per_row, to = sh.place[q];
+                int q = tid / per_row, c = tid - q * per_row;
+                const int dq = kAbThreads / per_row, dc = kAbThreads - dq * per_row;
+                for (; q < kRunRows; q += dq, c += dc) {
+                    if (c >= per_row) {
+                        c -= per_row;
+                        ++q;
+                        if (q >= kRunRows) break;
+                    }
+                    const int to = place[q];
                     if (to >= 0)
                         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool) + (int64_t)to * bytes + c * 16) =
                             *reinterpret_cast<const uint4*>(from + stage_at(q, c * 16, from_pitch));
@@ -385,12 +378,12 @@ __global__ void __launch_bounds__(kAbThreads, 1) k_append_basis(const AppendArgs
             else copy_out(A, 128 * E::kBytes, a.K_pages, D * E::kBytes);
             if (lo_bytes > 0 && staged) copy_out(A, pitch, a.plane, lo_bytes);
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            group_sync();  // A and place may be written again
+            __syncthreads();  // A and place may be written again
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if (tid < 32) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem_slot));
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem_slot));
 }
 
 template <class E, bool kQ8>
@@ -399,10 +392,11 @@ static cudaError_t basis_impl(const AppendArgs& a, cudaStream_t s) {
     DevInfo di;
     cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbSmem);
+    const int smem = kAbSmem + (a.rope != nullptr ? kRunRows * a.rot_dim * 4 : 0);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbSmem + kRunRows * 128 * 4);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (((int64_t)a.T + kRunRows - 2) / kRunRows + 1) * a.B * a.H_kv;
-    return launch_kernel(kern, dim3((unsigned)min64(tiles, di.sm_count)), dim3(kAbThreads), kAbSmem, s, false, a);
+    return launch_kernel(kern, dim3((unsigned)min64(tiles, di.sm_count)), dim3(kAbThreads), smem, s, false, a);
 }
 
 cudaError_t launch_append_basis(Dt dt, const AppendArgs& a, cudaStream_t s) {

@@ -196,8 +196,9 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_s
             }
         }
     }
-    // as a programmatic dependent of the keys' kernel: end after it
-    griddep_wait();
+    // A programmatic dependent of the keys' kernel, which it shares no data with: the grid must end
+    // after it, so one CTA waits (the others would hold their places on the SMs).
+    if (blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 
 template <class E, bool kQ8>
