@@ -90,14 +90,15 @@ __device__ __forceinline__ int stage_at(int r, int at, int pitch) { return r * p
 template <class E, int D, bool kQ8>
 __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_basis(const AppendArgs a) {
     using Tp = typename E::T;
-    constexpr int DH = D / 2;  // an epilogue thread's columns, and a thread's rows of P
+    constexpr int DH = D / 2;               // an epilogue thread's columns, and a thread's rows of P
+    constexpr int DC = D == 128 ? 32 : 16;  // of the columns at a time
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) float col_down[128];
     __shared__ float col_top[2][128];
     __shared__ float row_down[kRunRows], red[2][kRunRows / 16];
     __shared__ int place[kRunRows];  // the tile's rows in the pool, -1: not written
     __shared__ uint8_t odd_row[kRunRows];
-    __shared__ __align__(8) uint64_t bar, angle_bar;
+    __shared__ __align__(8) uint64_t bar, angle_bar, basis_bar;
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* Bm = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
     if (tid == 0) {
         mbar_init(&bar, 1);
         mbar_init(&angle_bar, 1);
+        mbar_init(&basis_bar, 1);
         fence_mbar_init();
     }
     // this CTA's tiles: heads slowest, then sequences, then their runs
@@ -159,43 +161,59 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
 
     uint32_t phase = 0;
     bool alive = true;
+    uint32_t heads = 0;
     int64_t ri = 0;  // w's place under its head
     if (w < w_end) {
         hk = (int)quot(w, R);
         ri = w - hk * R;
     }
-    for (; w < w_end; ++hk, ri = 0) {  // head by head
+    for (; alive && w < w_end; ++hk, ri = 0) {  // head by head
         int64_t left = min64(w_end - w, R - ri);  // tiles under this head
         w += left;
-        {
-            int64_t before;
-            b = seqs_find(a.B, ri, 1, runs_of, &before);
-            sq = append_seq(a, b, false);
-            runs = run_count(sq.lo, sq.hi);
-            run = (int)(ri - before);
-            load();
+        // P, as it is, to where A will be; two threads to a column, half of its rows each: the largest
+        // magnitude, then the parts
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();  // the last head's product and staged rows are done with
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&basis_bar, D * D * 4);
+            bulk_load(A, a.P + (int64_t)hk * D * D, D * D * 4, &basis_bar);
         }
-        __syncthreads();  // no product reads the last head's P any more
+        int64_t before;
+        b = seqs_find(a.B, ri, 1, runs_of, &before);
+        sq = append_seq(a, b, false);
+        runs = run_count(sq.lo, sq.hi);
+        run = (int)(ri - before);
+        load();
         {
-            // two threads to a column, half of its rows each: the largest magnitude, then the parts
+            if (!mbar_wait(&basis_bar, heads & 1, a.err)) alive = false;
+            ++heads;
             const int c = tid & 127, i0 = (tid >> 7) * DH;
-            float x[DH], top = 0.f;
+            const float* Ph = reinterpret_cast<const float*>(A) + i0 * D + c;
+            float top = 0.f;
             if (c < D) {
-                const float* Ph = a.P + (int64_t)hk * D * D + i0 * D + c;
+                float x[16];
+#pragma unroll 1
+                for (int i = 0; i < DH; i += 16) {
 #pragma unroll
-                for (int i = 0; i < DH; ++i) x[i] = __ldg(Ph + i * D);
-                top = finite_amax<DH>(0.f, x);
+                    for (int k = 0; k < 16; ++k) x[k] = Ph[(i + k) * D];
+                    top = finite_amax<16>(top, x);
+                }
             }
             col_top[tid >> 7][c] = top;
             __syncthreads();
             const int e = lift(fmaxf(col_top[0][c], col_top[1][c]));
             if (tid < 128) col_down[c] = pow2(-e);
             if (c < D) {
+                float x[8];
+#pragma unroll 2
+                for (int i = 0; i < DH; i += 8) {
 #pragma unroll
-                for (int i = 0; i < DH; i += 8) put_parts(Bm, c, i0 + i, x + i, pow2(e));
+                    for (int k = 0; k < 8; ++k) x[k] = Ph[(i + k) * D];
+                    put_parts(Bm, c, i0 + i, x, pow2(e));
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
+            alive = !__syncthreads_or(!alive);
         }
         for (; alive && left > 0; --left) {
             const int64_t start = (sq.lo / kRunRows + run) * kRunRows, lo = sq.lo, hi = sq.hi, p0 = sq.p0;
@@ -279,12 +297,13 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
             const uint32_t cols = tmem + ((uint32_t)(warp & 3) << 21);
             const float down = row_down[r];
             const bool odd = mine && odd_row[r];
-            // columns c .. c + 15 of the row, times f / down
+            // columns c .. c + DC - 1 of the row, times f / down
             auto columns = [&](int c, float* y, float f) {
-                tmem_ld16(y, cols + c);
+#pragma unroll
+                for (int i = 0; i < DC; i += 16) tmem_ld16(y + i, cols + c + i);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
+                for (int i = 0; i < DC; i += 4) {
                     const float4 cd = *reinterpret_cast<const float4*>(&col_down[c + i]);
                     y[i] = y[i] * cd.x * f;
                     y[i + 1] = y[i + 1] * cd.y * f;
@@ -295,15 +314,15 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
                 const Tp* K = static_cast<const Tp*>(a.K_new) + (((int64_t)tb * a.H_kv + hk) * a.T + (j - p0)) * D;
                 const float* Ph = a.P + (int64_t)hk * D * D + c;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = 0.f;
+                for (int i = 0; i < DC; ++i) y[i] = 0.f;
 #pragma unroll 1
                 for (int i = 0; i < D; ++i) {
                     const float x = turned_col<E>(a, K, j, i);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = fmaf(x, __ldg(Ph + i * D + e), y[e]);
+                    for (int e = 0; e < DC; ++e) y[e] = fmaf(x, __ldg(Ph + i * D + e), y[e]);
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] *= f;  // (an odd row's down is 1)
+                for (int i = 0; i < DC; ++i) y[i] *= f;  // (an odd row's down is 1)
             };
             // The tile's outputs go into A, whose product is done: rows of the cache's type (8 bits: of the
             // plane, as far as they fit in front of the codes).
@@ -313,20 +332,20 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
             const bool staged = !kQ8 || pitch * kRunRows <= 3 * kAbAtom;
             float top = 0.f;
 #pragma unroll
-            for (int c = c0; c < c0 + DH; c += 16) {
-                float y[16];
+            for (int c = c0; c < c0 + DH; c += DC) {
+                float y[DC];
                 columns(c, y, down);
                 if (!kQ8 || (c < a.d_lo && staged)) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += E::kVec)
+                    for (int i = 0; i < DC; i += E::kVec)
                         if (!kQ8 || c + i < a.d_lo)
                             *reinterpret_cast<uint4*>(A + stage_at(r, (c + i) * E::kBytes, pitch)) = pack16(y + i, E());
                 } else if (write && c < a.d_lo) {
                     Tp* o = static_cast<Tp*>(a.plane) + (int64_t)row * a.d_lo + c;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8) store_chunk<E>(o + i, y + i, c + i, a.d_lo);
+                    for (int i = 0; i < DC; i += 8) store_chunk<E>(o + i, y + i, c + i, a.d_lo);
                 }
-                if (kQ8 && mine) top = finite_amax<16>(top, y);
+                if (kQ8 && mine) top = finite_amax<DC>(top, y);
             }
             if constexpr (kQ8) {
 #pragma unroll
@@ -344,11 +363,14 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
                 const float grown = pow2_scale(top), s = has_old ? fmaxf(old, grown) : grown;
                 const float f = fminf(down * (1.f / s), 3.402823466e38f);
 #pragma unroll
-                for (int c = c0; c < c0 + DH; c += 16) {
-                    float y[16];
+                for (int c = c0; c < c0 + DH; c += DC) {
+                    float y[DC];
                     columns(c, y, f);
-                    const uint2 p = codes8(y, 1.f), q = codes8(y + 8, 1.f);
-                    *reinterpret_cast<uint4*>(stage8 + stage_at(r, c, 128)) = make_uint4(p.x, p.y, q.x, q.y);
+#pragma unroll
+                    for (int i = 0; i < DC; i += 16) {
+                        const uint2 p = codes8(y + i, 1.f), q = codes8(y + i + 8, 1.f);
+                        *reinterpret_cast<uint4*>(stage8 + stage_at(r, c + i, 128)) = make_uint4(p.x, p.y, q.x, q.y);
+                    }
                 }
                 if (!write && row >= 0 && has_old && s > old) {
                     uint32_t* v = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.K_pages) + (int64_t)row * D + c0);
