@@ -9,12 +9,12 @@ namespace loki {
 // ---------------------------------------------------------------------------
 // Longer appends as streams, one read and one write of each row. Bytes bound
 // them, and what the loads in flight cost is registers: values and queries
-// share a kernel of 24 warps an SM, keys without a basis, which are turned and
-// then scaled, have one of their own with 16.
+// share a kernel of up to 24 warps an SM; keys without a basis, which are turned
+// and then scaled, have one of their own, a CTA to an SM, which runs beside it.
 //
 // Values and keys: a CTA has an aligned run of 128 positions and goes through
 // some heads, a warp has 16 of the positions, eight lanes to a row (16 columns
-// each). 8-bit scale blocks of more than 16 tokens belong to neighbouring
+// each); the next head's rows are loaded before this one's are stored. 8-bit scale blocks of more than 16 tokens belong to neighbouring
 // warps, which share their largest magnitude through shared memory, so every
 // scale has one owner.
 // Queries: a warp has four positions, whose angles stay in its registers while
@@ -101,33 +101,39 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_s
     if ((int)blockIdx.x >= a.kv_ctas) {
         const int q = blockIdx.x - a.kv_ctas, chunk = q % a.q_chunks, rest = q / a.q_chunks, b = rest % a.B;
         const int t = rest / a.B * kStQueryRows + 4 * warp + sub;
+        const int h0 = chunk * a.q_group, h1 = min(h0 + a.q_group, a.H_q);
+        const bool here = lane_on && t < a.T;
+        int ca, cb;
+        const bool turn = a.rope != nullptr && u < a.rot_dim >> 4;
+        unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
+        const int64_t step = (int64_t)a.T * a.D, at = (((int64_t)b * a.H_q + h0) * a.T + t) * a.D;
+        const Tp* p = static_cast<const Tp*>(a.q) + at;
+        Tp* o = static_cast<Tp*>(a.q_out) + at;
+        // U heads are on their way; a head's registers take the one U behind it as soon as it is unpacked
+        constexpr int U = E::kBytes == 2 ? 4 : 2;
+        Chunk<E> wa[U], wb[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (here && h0 + i < h1) {
+                wa[i].load(p + i * step + ca);
+                wb[i].load(p + i * step + cb);
+            }
         const int64_t j = (int64_t)__ldg(a.positions + b) + t;
         const int n = a.new_lens != nullptr ? min(__ldg(a.new_lens + b), a.T) : a.T;
-        if (lane_on && t < n && j >= 0 && (a.rope == nullptr || j < a.n_pos)) {
-            const bool turn = a.rope != nullptr && u < a.rot_dim >> 4;
-            int ca, cb;
-            unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
+        if (here && t < n && j >= 0 && (a.rope == nullptr || j < a.n_pos)) {
             Angles g;
             if (turn) g.load(a.rope + j * a.rot_dim, a.rot_dim, u);
-            const int h0 = chunk * a.q_group, h1 = min(h0 + a.q_group, a.H_q);
-            const int64_t step = (int64_t)a.T * a.D, at = (((int64_t)b * a.H_q + h0) * a.T + t) * a.D;
-            const Tp* p = static_cast<const Tp*>(a.q) + at;
-            Tp* o = static_cast<Tp*>(a.q_out) + at;
-            constexpr int U = E::kBytes == 2 ? 4 : 2;
             for (int h = h0; h < h1; h += U) {
-                Chunk<E> wa[U], wb[U];
-#pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (h + i < h1) {
-                        wa[i].load(p + i * step + ca);
-                        wb[i].load(p + i * step + cb);
-                    }
 #pragma unroll
                 for (int i = 0; i < U; ++i)
                     if (h + i < h1) {
                         float x[16];
                         wa[i].get(x);
                         wb[i].get(x + 8);
+                        if (h + i + U < h1) {
+                            wa[i].load(p + (i + U) * step + ca);
+                            wb[i].load(p + (i + U) * step + cb);
+                        }
                         if (turn) g.turn(x, a.interleaved);
                         store_chunk<E>(o + i * step + ca, x, ca, a.D);
                         store_chunk<E>(o + i * step + cb, x + 8, cb, a.D);
@@ -147,15 +153,19 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_s
             const Tp* p = static_cast<const Tp*>(a.V_new) + ((int64_t)b * a.H_kv + h0) * step +
                           (pl.j0 - sq.p0 + sub) * a.D + 16 * u;
             int parity = 0;
-            for (int h = h0; h < h1; ++h, p += step) {
-                const int shift = h * a.page_size;
-                Chunk<E> w[4][2];
+            Chunk<E> w[4][2];
+            auto load = [&]() {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (pl.live >> i & 1u) {
                         w[i][0].load(p + 4 * i * a.D);
                         w[i][1].load(p + 4 * i * a.D + 8);
                     }
+                p += step;
+            };
+            load();
+            for (int h = h0; h < h1; ++h) {
+                const int shift = h * a.page_size;
                 if constexpr (!kQ8) {  // in their own type: copied, bit by bit
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -167,6 +177,7 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_s
                                 o[Chunk<E>::kN + e] = w[i][1].w[e];
                             }
                         }
+                    if (h + 1 < h1) load();
                 } else {
                     float amax = 0.f;
 #pragma unroll
@@ -182,15 +193,19 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_s
                     const float s = block_scale(a, amax, red[parity], sc, pl.has_old, &old), inv = 1.f / s;
                     parity ^= 1;
                     uint8_t* o = static_cast<uint8_t*>(a.V_pages) + (pl.at(0, shift) - sub) * a.D;
+                    uint4 y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x[16];
+                        w[i][0].get(x);
+                        w[i][1].get(x + 8);
+                        const uint2 ya = codes8(x, inv), yb = codes8(x + 8, inv);
+                        y[i] = make_uint4(ya.x, ya.y, yb.x, yb.y);
+                    }
+                    if (h + 1 < h1) load();
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (pl.live >> i & 1u) {
-                            float x[16];
-                            w[i][0].get(x);
-                            w[i][1].get(x + 8);
-                            const uint2 y = codes8(x, inv), z = codes8(x + 8, inv);
-                            *reinterpret_cast<uint4*>(o + (4 * i + sub) * a.D + 16 * u) = make_uint4(y.x, y.y, z.x, z.y);
-                        }
+                        if (pl.live >> i & 1u) *reinterpret_cast<uint4*>(o + (4 * i + sub) * a.D + 16 * u) = y[i];
                     if (sc != nullptr && pl.has_old && s > old) rescale_rows(a, o, pl.j0, sq.lo, old / s);
                 }
             }
@@ -206,76 +221,96 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
     using Tp = typename E::T;
     extern __shared__ __align__(16) float angles[];  // the run's, [128][rot_dim]
     __shared__ float red[2][kStThreads / 32];
+    __shared__ __align__(8) uint64_t bar;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
     const bool lane_on = u < a.D >> 4;
-    const int chunk = blockIdx.x % a.chunks, rest = blockIdx.x / a.chunks, b = rest % a.B;
     griddep_launch_dependents();
-    const ApSeq sq = append_seq(a, b, false);
-    const int64_t start = (sq.lo / kRunRows + rest / a.B) * kRunRows;
-    if (start >= sq.hi) return;
-    const int rot = a.rope != nullptr ? a.rot_dim : 0;
-    if (rot > 0) {
-        const int n = (int)min64(sq.hi - start, kRunRows) * (rot >> 2);
-        const int skip = (int)(sq.lo > start ? sq.lo - start : 0) * (rot >> 2);
-        for (int i = skip + threadIdx.x; i < n; i += kStThreads)
-            reinterpret_cast<float4*>(angles)[i] = __ldg(reinterpret_cast<const float4*>(a.rope + start * rot) + i);
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
     }
-    const RunPlace<kQ8> pl(a, sq, b, start, lane_on);
+    const int rot = a.rope != nullptr ? a.rot_dim : 0;
     const bool turn = u < rot >> 4;
     int ca, cb;
     unit_cols(turn ? rot : 0, a.interleaved, u, &ca, &cb);
-    const int h0 = chunk * a.group, h1 = min(h0 + a.group, a.H_kv);
-    const int64_t step = (int64_t)a.T * a.D;
-    const Tp* p = static_cast<const Tp*>(a.K_new) + ((int64_t)b * a.H_kv + h0) * step + (pl.j0 - sq.p0 + sub) * a.D;
-    Chunk<E> wa[4], wb[4];
-    auto load = [&]() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (pl.live >> i & 1u) {
-                wa[i].load(p + 4 * i * a.D + ca);
-                wb[i].load(p + 4 * i * a.D + cb);
-            }
-        p += step;
+    auto runs_of = [&](int b) -> int64_t {
+        const ApSeq s = append_seq(a, b, false);
+        return run_count(s.lo, s.hi);
     };
-    load();
-    __syncthreads();  // the angles
+    const int64_t total = seqs_total(a.B, runs_of) * a.H_kv, per = quot(total + gridDim.x - 1, gridDim.x);
+    int64_t w = min64(blockIdx.x * per, total);
+    const int64_t w_end = min64(w + per, total), step = (int64_t)a.T * a.D;
     int parity = 0;
-    for (int h = h0; h < h1; ++h) {
-        const int shift = h * a.page_size;
-        float x[4][16], amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            wa[i].get(x[i]);
-            wb[i].get(x[i] + 8);
-            if (turn) turn_unit_from(angles + (16 * warp + 4 * i + sub) * rot, rot, a.interleaved, u, x[i]);
-            if (!(pl.live >> i & 1u)) continue;
-            if (a.plane != nullptr) {
-                Tp* o = static_cast<Tp*>(a.plane) + pl.at(i, shift) * a.d_lo;
-                store_chunk<E>(o + ca, x[i], ca, a.d_lo);
-                store_chunk<E>(o + cb, x[i] + 8, cb, a.d_lo);
-            }
-            if constexpr (!kQ8) {
-                Tp* o = static_cast<Tp*>(a.K_pages) + pl.at(i, shift) * a.D;
-                store_chunk<E>(o + ca, x[i], ca, a.D);
-                store_chunk<E>(o + cb, x[i] + 8, cb, a.D);
-            } else {
-                amax = finite_amax<16>(amax, x[i]);
-            }
+    uint32_t phase = 0;
+    while (w < w_end) {  // run by run, heads fastest
+        const int64_t ri = quot(w, a.H_kv);
+        int64_t before;
+        const int b = seqs_find(a.B, ri, 1, runs_of, &before);
+        const int h0 = (int)(w - ri * a.H_kv), h1 = (int)min64(a.H_kv, h0 + (w_end - w));
+        w += h1 - h0;
+        const ApSeq sq = append_seq(a, b, false);
+        const int64_t start = (sq.lo / kRunRows + (ri - before)) * kRunRows;
+        __syncthreads();  // the run before is done with its angles (and the barrier is set up)
+        if (rot > 0 && threadIdx.x == 0) {
+            const uint32_t bytes = (uint32_t)min64(sq.hi - start, kRunRows) * rot * 4;
+            mbar_arrive_expect_tx(&bar, bytes);
+            bulk_load(angles, a.rope + start * rot, bytes, &bar);
         }
-        if (h + 1 < h1) load();
-        if constexpr (kQ8) {
-            float old;
-            float* sc = pl.row[0] < 0 ? nullptr : a.k_scales + ((pl.row[0] + shift) >> a.block_log2);
-            const float s = block_scale(a, amax, red[parity], sc, pl.has_old, &old), inv = 1.f / s;
-            parity ^= 1;
-            uint8_t* o = static_cast<uint8_t*>(a.K_pages) + (pl.at(0, shift) - sub) * a.D;
+        const RunPlace<kQ8> pl(a, sq, b, start, lane_on);
+        const Tp* p = static_cast<const Tp*>(a.K_new) + ((int64_t)b * a.H_kv + h0) * step + (pl.j0 - sq.p0 + sub) * a.D;
+        Chunk<E> wa[4], wb[4];
+        auto load = [&]() {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (pl.live >> i & 1u) {
-                    *reinterpret_cast<uint2*>(o + (4 * i + sub) * a.D + ca) = codes8(x[i], inv);
-                    *reinterpret_cast<uint2*>(o + (4 * i + sub) * a.D + cb) = codes8(x[i] + 8, inv);
+                    wa[i].load(p + 4 * i * a.D + ca);
+                    wb[i].load(p + 4 * i * a.D + cb);
                 }
-            if (sc != nullptr && pl.has_old && s > old) rescale_rows(a, o, pl.j0, sq.lo, old / s);
+            p += step;
+        };
+        load();
+        if (rot > 0) {
+            const bool ok = mbar_wait(&bar, phase, a.err);
+            phase ^= 1;
+            if (__syncthreads_or(!ok)) return;
+        }
+        for (int h = h0; h < h1; ++h) {
+            const int shift = h * a.page_size;
+            float x[4][16], amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wa[i].get(x[i]);
+                wb[i].get(x[i] + 8);
+                if (turn) turn_unit_from(angles + (16 * warp + 4 * i + sub) * rot, rot, a.interleaved, u, x[i]);
+                if (!(pl.live >> i & 1u)) continue;
+                if (a.plane != nullptr) {
+                    Tp* o = static_cast<Tp*>(a.plane) + pl.at(i, shift) * a.d_lo;
+                    store_chunk<E>(o + ca, x[i], ca, a.d_lo);
+                    store_chunk<E>(o + cb, x[i] + 8, cb, a.d_lo);
+                }
+                if constexpr (!kQ8) {
+                    Tp* o = static_cast<Tp*>(a.K_pages) + pl.at(i, shift) * a.D;
+                    store_chunk<E>(o + ca, x[i], ca, a.D);
+                    store_chunk<E>(o + cb, x[i] + 8, cb, a.D);
+                } else {
+                    amax = finite_amax<16>(amax, x[i]);
+                }
+            }
+            if (h + 1 < h1) load();
+            if constexpr (kQ8) {
+                float old;
+                float* sc = pl.row[0] < 0 ? nullptr : a.k_scales + ((pl.row[0] + shift) >> a.block_log2);
+                const float s = block_scale(a, amax, red[parity], sc, pl.has_old, &old), inv = 1.f / s;
+                parity ^= 1;
+                uint8_t* o = static_cast<uint8_t*>(a.K_pages) + (pl.at(0, shift) - sub) * a.D;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (pl.live >> i & 1u) {
+                        *reinterpret_cast<uint2*>(o + (4 * i + sub) * a.D + ca) = codes8(x[i], inv);
+                        *reinterpret_cast<uint2*>(o + (4 * i + sub) * a.D + cb) = codes8(x[i] + 8, inv);
+                    }
+                if (sc != nullptr && pl.has_old && s > old) rescale_rows(a, o, pl.j0, sq.lo, old / s);
+            }
         }
     }
 }
@@ -566,15 +601,12 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
     if (a.P != nullptr) {
         e = launch_append_basis(E::kBytes == 4 ? kF32 : kBF16, a, s);
     } else {
-        AppendArgs k = a;
-        k.group = heads_per_cta(runs, a.H_kv, E::kBytes == 2 ? 2 : 1, 3);
-        k.chunks = (a.H_kv + k.group - 1) / k.group;
-        if (runs * k.chunks > 0x7fffffff) return cudaErrorInvalidValue;
+        // one CTA to an SM, which leaves half of its registers to the stream
         auto kern = k_append_keys<E, kQ8>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunRows * 128 * 4);
         if (e != cudaSuccess) return e;
         const size_t smem = a.rope != nullptr ? (size_t)kRunRows * a.rot_dim * sizeof(float) : 0;
-        e = launch_kernel(kern, dim3((unsigned)(runs * k.chunks)), dim3(kStThreads), smem, s, false, k);
+        e = launch_kernel(kern, dim3((unsigned)min64(runs * a.H_kv, di.sm_count)), dim3(kStThreads), smem, s, false, a);
     }
     if (e != cudaSuccess) return e;
     const int per_sm = E::kBytes == 2 ? 3 : 2;
