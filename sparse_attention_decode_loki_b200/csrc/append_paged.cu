@@ -93,14 +93,15 @@ __device__ __forceinline__ void rescale_rows(const AppendArgs& a, uint8_t* codes
 }
 
 template <class E, bool kQ8>
-__global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_stream(const AppendArgs a) {
+__global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_stream(const AppendArgs a) {
     using Tp = typename E::T;
     __shared__ float red[2][kStThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
     const bool lane_on = u < a.D >> 4;
     if ((int)blockIdx.x >= a.kv_ctas) {
-        const int q = blockIdx.x - a.kv_ctas, chunk = q % a.q_chunks, rest = q / a.q_chunks, b = rest % a.B;
-        const int t = rest / a.B * kStQueryRows + 4 * warp + sub;
+        // CTAs side by side take rows side by side
+        const int q = blockIdx.x - a.kv_ctas, blocks = (a.T + kStQueryRows - 1) / kStQueryRows, b = q / blocks % a.B;
+        const int t = q % blocks * kStQueryRows + 4 * warp + sub, chunk = q / blocks / a.B;
         const int h0 = chunk * a.q_group, h1 = min(h0 + a.q_group, a.H_q);
         const bool here = lane_on && t < a.T;
         int ca, cb;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 3 : 2) k_append_s
         const Tp* p = static_cast<const Tp*>(a.q) + at;
         Tp* o = static_cast<Tp*>(a.q_out) + at;
         // U heads are on their way; a head's registers take the one U behind it as soon as it is unpacked
-        constexpr int U = E::kBytes == 2 ? 4 : 2;
+        constexpr int U = 2;
         Chunk<E> wa[U], wb[U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -609,7 +610,7 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
         e = launch_kernel(kern, dim3((unsigned)min64(runs * a.H_kv, di.sm_count)), dim3(kStThreads), smem, s, false, a);
     }
     if (e != cudaSuccess) return e;
-    const int per_sm = E::kBytes == 2 ? 3 : 2;
+    const int per_sm = E::kBytes == 2 ? 4 : 2;
     a.group = heads_per_cta(runs, a.H_kv, per_sm, 3);
     a.chunks = (a.H_kv + a.group - 1) / a.group;
     int64_t q_ctas = 0;
