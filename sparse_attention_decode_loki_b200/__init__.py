@@ -19,6 +19,7 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import DTYPE_BF16, DTYPE_F32, LIB_PATH, LokiError, check, lib  # noqa: F401
+from . import _binding as _b  # built beside libloki.so by build.py
 
 __all__ = [
     "LokiError", "LIB_PATH",
@@ -367,21 +368,8 @@ def loki_append_keys_paged(K_new: torch.Tensor, V_new: torch.Tensor, P: torch.Te
 # paged appends with the rotary embedding, 8-bit pages
 # ---------------------------------------------------------------------------
 
-def _place(*ts: torch.Tensor) -> int:
-    """The CUDA device index that contiguous tensors share (_cuda's checks, without device objects:
-    a decode step's calls are short enough for the host's side to count)."""
-    i = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != i or not t.is_contiguous():
-            _cuda(*ts)
-    if i < 0:
-        _cuda(*ts)
-    return i
-
-
-def _launch(name: str, i: int, args: tuple) -> None:
-    """Calls the library's `name` on device i's current stream, with i as the current device."""
-    f = getattr(lib, name)
+def _launch(f, name: str, i: int, *args) -> None:
+    """Calls the library's entry on device i's current stream, with i as the current device."""
     if torch.cuda.current_device() == i:
         status = f(*args, _raw_stream(i))
     else:
@@ -399,17 +387,17 @@ def loki_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, pos_scale: 
     if table is None:
         table = torch.empty((n_pos, rot_dim), dtype=torch.float32,
                             device="cuda" if device is None else device)
-    i = _place(table)
+    i = _b.place(table)
     _expect(table, (n_pos, rot_dim), torch.float32, "table")
-    _launch("loki_rope_table", i, (table.data_ptr(), n_pos, rot_dim, base, pos_scale))
+    _launch(_b.loki_rope_table, "loki_rope_table", i, table, n_pos, rot_dim, base, pos_scale)
     return table
 
 
 def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rope_table, plane,
                   new_lens, q, q_out, *scales):
     """What the two rotary appends share: (device index, H_q, q_out, the C arguments around the pages)."""
-    i = _place(K_new, V_new, K_pages, V_pages, block_table, positions, *scales,
-               *[t for t in (P, rope_table, plane, new_lens, q, q_out) if t is not None])
+    i = _b.place(K_new, V_new, K_pages, V_pages, block_table, positions, P, rope_table, plane,
+                 new_lens, q, q_out, *scales)
     ks, ps, bs, dtype = K_new.shape, K_pages.shape, block_table.shape, K_new.dtype
     if len(ks) != 4 or len(ps) != 4 or len(bs) != 2:
         raise ValueError("K_new [B, H_kv, T, D], pages [n_pages, H_kv, page_size, D] and "
@@ -431,7 +419,7 @@ def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rop
     if rope_table is not None:
         if rope_table.dim() != 2 or rope_table.dtype != torch.float32:
             raise ValueError("rope_table must be float32 [n_pos, rot_dim]")
-        table = (rope_table.data_ptr(), *rope_table.shape)
+        table = (rope_table, *rope_table.shape)
     d_lo = 0
     if plane is not None:
         if plane.dim() != 4:
@@ -447,16 +435,13 @@ def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rop
         H_q = q.shape[1]
         _expect(q, (B, H_q, T, D), dtype, "q")
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _b.empty_like(q)
         else:
             _expect(q_out, q.shape, q.dtype, "q_out")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    front = (K_new.data_ptr(), V_new.data_ptr(), None if P is None else P.data_ptr(), *table)
-    back = (None if plane is None else plane.data_ptr(), d_lo, block_table.data_ptr(),
-            positions.data_ptr(), None if new_lens is None else new_lens.data_ptr(), B, H_kv, T,
-            page_size, bs[1], n_pages, D, dt)
-    return i, H_q, q_out, front, back
+    return (i, H_q, q_out, (K_new, V_new, P, *table),
+            (plane, d_lo, block_table, positions, new_lens, B, H_kv, T, page_size, bs[1], n_pages, D, dt))
 
 
 def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
@@ -476,9 +461,8 @@ def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Opt
                                                positions, rope_table, Kt_lo_pages, new_lens, q, q_out)
     if Kt_pages.dtype != K_new.dtype:
         raise TypeError("K_new and the pages must share a dtype")
-    _launch("loki_append_keys_paged_rope", i,
-            (*front, int(interleaved), None if q is None else q.data_ptr(),
-             None if q is None else q_out.data_ptr(), H_q, Kt_pages.data_ptr(), V_pages.data_ptr(), *back))
+    _launch(_b.loki_append_keys_paged_rope, "loki_append_keys_paged_rope", i, *front,
+            bool(interleaved), q, q_out, H_q, Kt_pages, V_pages, *back)
     return q_out
 
 
@@ -514,10 +498,8 @@ def loki_append_keys_paged_q8(K_new: torch.Tensor, V_new: torch.Tensor, P: Optio
     i, H_q, q_out, front, back = _check_append(K_new, V_new, P, K8_pages, V8_pages, block_table,
                                                positions, rope_table, Kt_lo_pages, new_lens, q, q_out,
                                                k_scales, v_scales)
-    _launch("loki_append_keys_paged_q8", i,
-            (*front, int(interleaved), None if q is None else q.data_ptr(),
-             None if q is None else q_out.data_ptr(), H_q, K8_pages.data_ptr(), V8_pages.data_ptr(),
-             k_scales.data_ptr(), v_scales.data_ptr(), block, *back))
+    _launch(_b.loki_append_keys_paged_q8, "loki_append_keys_paged_q8", i, *front, bool(interleaved),
+            q, q_out, H_q, K8_pages, V8_pages, k_scales, v_scales, block, *back)
     return q_out
 
 
@@ -540,8 +522,7 @@ def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq
     """What the attentions over 8-bit pages share: (device index, the sizes B, H_q, H_kv, page_size,
     max_pages, n_pages, D of the C calls, the C arguments in front of their own)."""
     block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
-    i = _place(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens,
-               *[t for t in more if t is not None])
+    i = _b.place(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, *more)
     n_pages, H_kv, page_size, D = K8_pages.shape
     qs, bs = q.shape, block_table.shape
     if len(qs) != 3 or len(bs) != 2:
@@ -551,9 +532,7 @@ def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq
         raise ValueError("q [B, H_q, D], block_table [B, max_pages], seq_lens [B] disagree")
     if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_table and seq_lens must be int32")
-    front = (q.data_ptr(), K8_pages.data_ptr(), V8_pages.data_ptr(), k_scales.data_ptr(),
-             v_scales.data_ptr(), block)
-    return i, (B, H_q, H_kv, page_size, bs[1], n_pages, D), front
+    return i, (B, H_q, H_kv, page_size, bs[1], n_pages, D), (q, K8_pages, V8_pages, k_scales, v_scales, block)
 
 
 _dense_q8_ws = functools.lru_cache(maxsize=1024)(dense_decode_paged_q8_workspace_size)
@@ -573,13 +552,14 @@ def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
                                        seq_lens, out, workspace)
     B, H_q, H_kv, page_size, max_pages, _, D = sizes
     if out is None:
-        out = torch.empty_like(q)
+        out = _b.empty_like(q)
     else:
         _expect(out, q.shape, q.dtype, "out")
-    ws = _ws(_dense_q8_ws(B, H_q, H_kv, page_size, max_pages, D), q.device, workspace)
-    _launch("dense_decode_attention_paged_q8", i,
-            (*front, block_table.data_ptr(), seq_lens.data_ptr(), *sizes, scale, _dt(q),
-             out.data_ptr(), ws.data_ptr(), _ws_bytes(ws)))
+    ws = workspace
+    if ws is None:
+        ws = _b.scratch(q, _dense_q8_ws(B, H_q, H_kv, page_size, max_pages, D))
+    _launch(_b.dense_decode_attention_paged_q8, "dense_decode_attention_paged_q8", i, *front,
+            block_table, seq_lens, *sizes, scale, _dt(q), out, ws, ws.nbytes)
     return out
 
 
@@ -602,13 +582,14 @@ def loki_sparse_attention_paged_q8(q_rot: torch.Tensor, K8_pages: torch.Tensor,
     k = selected_idx.shape[2]
     _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
     if out is None:
-        out = torch.empty((B, H_q, D), dtype=dtype, device=q_rot.device)
+        out = _b.empty_like(q_rot, dtype)
     else:
         _expect(out, (B, H_q, D), out.dtype, "out")
-    ws = _ws(_sparse_q8_ws(B, H_q, H_kv, k, D), q_rot.device, workspace)
-    _launch("loki_sparse_attention_paged_q8", i,
-            (*front, block_table.data_ptr(), seq_lens.data_ptr(), selected_idx.data_ptr(), *sizes, k,
-             scale, _dt(out), out.data_ptr(), ws.data_ptr(), _ws_bytes(ws)))
+    ws = workspace
+    if ws is None:
+        ws = _b.scratch(q_rot, _sparse_q8_ws(B, H_q, H_kv, k, D))
+    _launch(_b.loki_sparse_attention_paged_q8, "loki_sparse_attention_paged_q8", i, *front,
+            block_table, seq_lens, selected_idx, *sizes, k, scale, _dt(out), out, ws, ws.nbytes)
     return out
 
 
@@ -631,16 +612,17 @@ def loki_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor, V8_p
     _expect(Kt_lo_pages, (n_pages, H_kv, page_size, d_lo), q.dtype, "Kt_lo_pages")
     _expect(P, (H_kv, D, D), torch.float32, "P")
     if out is None:
-        out = torch.empty_like(q)
+        out = _b.empty_like(q)
     if selected_idx is None:
         selected_idx = torch.empty((B, H_q, k), dtype=torch.int32, device=q.device)
     _expect(out, q.shape, q.dtype, "out")
     _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
-    ws = _ws(_decode_q8_ws(B, H_q, H_kv, page_size, max_pages, D, d, k), q.device, workspace)
-    _launch("loki_decode_attention_paged_q8", i,
-            (*front, Kt_lo_pages.data_ptr(), d_lo, P.data_ptr(), block_table.data_ptr(),
-             seq_lens.data_ptr(), *sizes, d, k, scale, _dt(q), out.data_ptr(),
-             selected_idx.data_ptr(), ws.data_ptr(), _ws_bytes(ws)))
+    ws = workspace
+    if ws is None:
+        ws = _b.scratch(q, _decode_q8_ws(B, H_q, H_kv, page_size, max_pages, D, d, k))
+    _launch(_b.loki_decode_attention_paged_q8, "loki_decode_attention_paged_q8", i, *front,
+            Kt_lo_pages, d_lo, P, block_table, seq_lens, *sizes, d, k, scale, _dt(q), out,
+            selected_idx, ws, ws.nbytes)
     return out, selected_idx
 
 

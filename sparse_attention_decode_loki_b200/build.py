@@ -7,7 +7,7 @@ is what this script produces.)
 
 Each .cu under csrc/ compiles to an object in _build/ (in parallel), then the
 objects link into sparse_attention_decode_loki_b200/libloki.so with the CUDA
-runtime linked statically. ptxas resource usage (registers, spills, shared
+runtime linked statically; csrc/binding.cpp compiles to _binding.so beside it. ptxas resource usage (registers, spills, shared
 memory) of every kernel goes to _build/ptxas.log.
 """
 from __future__ import annotations
@@ -17,12 +17,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libloki.so")
+BINDING = os.path.join(PKG, "_binding.so")  # Python's calls of the decode step's entries
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -79,9 +81,31 @@ def build(verbose: bool = False, force: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    build_binding(force)
     if verbose:
         print("\n".join(logs))
     return LIB
+
+
+def build_binding(force: bool = False) -> None:
+    """csrc/binding.cpp against this interpreter and its torch, next to libloki.so."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(ROOT, "include", "loki.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return
+    import torch  # for its headers' place and its ABI
+    home = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", src, "-o", BINDING,
+           "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(shutil.which(_nvcc()) or _nvcc())), "include"),
+           "-L", PKG, "-l:libloki.so", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
 
 
 if __name__ == "__main__":

@@ -415,7 +415,7 @@ static cudaError_t basis_impl(const AppendArgs& a, cudaStream_t s) {
     cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
     const int smem = kAbSmem + (a.rope != nullptr ? kRunRows * a.rot_dim * 4 : 0);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbSmem + kRunRows * 128 * 4);
+    e = allow_dynamic_smem((const void*)kern, kAbSmem + kRunRows * 128 * 4);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (((int64_t)a.T + kRunRows - 2) / kRunRows + 1) * a.B * a.H_kv;
     return launch_kernel(kern, dim3((unsigned)min64(tiles, di.sm_count)), dim3(kAbThreads), smem, s, false, a);

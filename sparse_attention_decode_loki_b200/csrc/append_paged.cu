@@ -604,7 +604,7 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
     } else {
         // one CTA to an SM, which leaves half of its registers to the stream
         auto kern = k_append_keys<E, kQ8>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRunRows * 128 * 4);
+        e = allow_dynamic_smem((const void*)kern, kRunRows * 128 * 4);
         if (e != cudaSuccess) return e;
         const size_t smem = a.rope != nullptr ? (size_t)kRunRows * a.rot_dim * sizeof(float) : 0;
         e = launch_kernel(kern, dim3((unsigned)min64(runs * a.H_kv, di.sm_count)), dim3(kStThreads), smem, s, false, a);

@@ -877,8 +877,7 @@ size_t sparse_q8_ws_bytes(int B, int H_q, int64_t k, int D) {
 // the kernel's dynamic shared memory and the largest shared split, set once
 static cudaError_t allow_smem(const void* f, size_t bytes) {
     const cudaError_t e = prefer_carveout(f, cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess || bytes <= 48 * 1024) return e;
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return e != cudaSuccess ? e : allow_dynamic_smem(f, bytes);
 }
 
 // CTAs of a cluster: as many as keep all clusters resident together, while

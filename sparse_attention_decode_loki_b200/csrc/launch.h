@@ -20,6 +20,8 @@ cudaError_t dev_info(DevInfo* out);
 
 // resident CTAs per SM of `func` at `threads` threads and `smem` dynamic bytes (cached)
 int occupancy(const void* func, int threads, size_t smem);
+// lets `func` use `bytes` of dynamic shared memory on the current device (cached)
+cudaError_t allow_dynamic_smem(const void* func, size_t bytes);
 
 // device address of this device's kernel error word (cached; null on failure)
 int* device_error_word();

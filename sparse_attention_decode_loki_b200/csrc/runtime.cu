@@ -2,6 +2,7 @@
 // resident-CTA count of each kernel instantiation. Grids are sized as
 // (SM count x resident CTAs per SM) so every CTA of a persistent split runs in
 // a single wave.
+#include <map>
 #include <mutex>
 #include <set>
 #include <unordered_map>
@@ -38,6 +39,7 @@ struct OccHash {
 };
 std::unordered_map<OccKey, int, OccHash> g_occ;
 std::set<std::pair<int, const void*>> g_carveout_set;
+std::map<std::pair<int, const void*>, size_t> g_smem_set;
 }  // namespace
 
 cudaError_t prefer_carveout(const void* func, int carveout) {
@@ -50,6 +52,19 @@ cudaError_t prefer_carveout(const void* func, int carveout) {
     if (e != cudaSuccess) return e;
     g_carveout_set.insert({dev, func});
     return cudaSuccess;
+}
+
+cudaError_t allow_dynamic_smem(const void* func, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(g_mu);
+    size_t& allowed = g_smem_set[{dev, func}];
+    if (allowed >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) allowed = bytes;
+    return e;
 }
 
 cudaError_t dev_info(DevInfo* out) {
