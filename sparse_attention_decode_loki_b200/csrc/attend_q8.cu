@@ -54,6 +54,10 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "launch.h"
 #include "q8.cuh"
 #include "seqs.cuh"
@@ -66,7 +70,7 @@ namespace cg = cooperative_groups;
 constexpr int kQ8Threads = 128;
 constexpr int kClThreads = 256;  // of the cluster kernels
 constexpr int kStages = 3;
-constexpr int kClusterTiles = 4;  // the most tiles a warp of theirs takes
+constexpr int kClusterTiles = 10;  // tiles for every resident warp up to which the clusters may be few
 constexpr int kQ8MaxWarps = 2 * 148 * 16;  // workspace is laid out for at most this many
 constexpr int kTile = 16;
 constexpr uint32_t kNoRow = 0xffffffffu;
@@ -880,13 +884,74 @@ static cudaError_t allow_smem(const void* f, size_t bytes) {
     return e != cudaSuccess ? e : allow_dynamic_smem(f, bytes);
 }
 
-// CTAs of a cluster: as many as keep all clusters resident together, while
-// every warp has a tile. 0: too many tiles a warp, the two-kernel form.
-static int cluster_size(int64_t units, int64_t tiles, int64_t resident) {
+static cudaLaunchConfig_t cluster_config(int64_t ctas, int cluster, size_t smem, cudaStream_t s,
+                                         cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kClThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = cluster;
+    attr->val.clusterDim.y = 1;
+    attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// clusters of 1 .. 8 CTAs of a cluster kernel that the device holds at a time
+// (whole clusters have to fit a group of SMs, so sizes like 7 lose places)
+struct ClusterSlots {
+    int active[9];
+};
+
+static cudaError_t cluster_slots(const void* kern, size_t smem, ClusterSlots* out) {
+    static std::mutex mu;
+    static std::map<std::pair<int, const void*>, ClusterSlots> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    const auto at = known.find({dev, kern});
+    if (at != known.end()) {
+        *out = at->second;
+        return cudaSuccess;
+    }
+    for (int c = 1; c <= 8; ++c) {
+        cudaLaunchAttribute attr[1];
+        cudaLaunchConfig_t cfg = cluster_config(c, c, smem, nullptr, attr);
+        e = cudaOccupancyMaxActiveClusters(&out->active[c], kern, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    known[{dev, kern}] = *out;
+    return cudaSuccess;
+}
+
+// CTAs of a unit's cluster, 0: the two-kernel form. The size that fills most
+// of the device while every warp has a tile. One kernel saves the
+// second launch and the partials' way through memory, 5 to 10 us; the equal
+// runs of the two-kernel form save the places that whole units leave empty.
+// Measured, us, cluster / two kernels (H_kv x sequences x tokens):
+//   40 x 16 x 4096 ragged 69 / 79, 8 x 4 x 32768 42 / 49, 32 x 4 x 2048 13 / 19;
+//   8 x 2 x 65536 (43 % of the places filled) 67 / 55, 40 x 8 x 4096 (54 %)
+//   75 / 63, 8 x 1 x 131072 (22 %) 114 / 75; 8 x 1 x 32768 (22 %, but few
+//   tiles) 32 / 38.
+static int cluster_size(int64_t units, int64_t tiles, const ClusterSlots& slots) {
     constexpr int W = kClThreads / 32;
-    int c = 8;
-    while (c > 1 && (units * c > resident || (c / 2) * W >= tiles)) c >>= 1;
-    return (tiles + c * W - 1) / (c * W) <= kClusterTiles ? c : 0;
+    const int64_t resident = slots.active[1];
+    int best = 1;
+    double fill = 0;
+    for (int c = 1; c <= 8 && (c == 1 || (c - 1) * W < tiles); ++c) {
+        if (slots.active[c] < 1 || (c > 1 && units > slots.active[c])) continue;
+        const int64_t waves = (units + slots.active[c] - 1) / slots.active[c];
+        const double f = (double)(units * c) / (double)(waves * resident);
+        if (f >= fill) {
+            fill = f;
+            best = c;
+        }
+    }
+    return fill >= 0.7 || units * tiles <= kClusterTiles * W * resident ? best : 0;
 }
 
 // the pages as a [rows, 128] byte matrix, in boxes of one tile
@@ -935,20 +1000,13 @@ static cudaError_t attend_impl(AttendQ8Args& a, cudaStream_t s) {
                               : (const void*)k_dense_q8<E, D, 2, true>;
     e = allow_smem(ck, csmem);
     if (e != cudaSuccess) return e;
-    a.cluster = cluster_size(units, tiles, (int64_t)di.sm_count * occupancy(ck, kClThreads, csmem));
+    ClusterSlots slots;
+    e = cluster_slots(ck, csmem, &slots);
+    if (e != cudaSuccess) return e;
+    a.cluster = cluster_size(units, tiles, slots);
     if (a.cluster > 0 && units * a.cluster <= 0x7fffffff) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(units * a.cluster));
-        cfg.blockDim = dim3(kClThreads);
-        cfg.dynamicSmemBytes = csmem;
-        cfg.stream = s;
         cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = a.cluster;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        const cudaLaunchConfig_t cfg = cluster_config(units * a.cluster, a.cluster, csmem, s, attr);
         void* args[] = {&a, &kmap, &vmap};
         return cudaLaunchKernelExC(&cfg, ck, args);
     }
