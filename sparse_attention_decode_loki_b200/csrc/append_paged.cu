@@ -376,19 +376,38 @@ __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) 
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     const bool lane_on = lane * 4 < D;
     if (mine) {
+        // the row's loads need no position: on their way before it is read
+        const int64_t at = (((int64_t)b * a.H_kv + hk) * a.T + t) * D;
+        const bool unit_on = lane < D >> 4, turn = unit_on && a.rope != nullptr && lane < a.rot_dim >> 4;
+        int ca, cb;
+        unit_cols(turn ? a.rot_dim : 0, a.interleaved, lane, &ca, &cb);
+        Chunk<E> wa, wb;
+        if (unit_on) {
+            wa.load(static_cast<const Tp*>(a.K_new) + at + ca);
+            wb.load(static_cast<const Tp*>(a.K_new) + at + cb);
+        }
+        if (lane_on) {
+            if constexpr (E::kBytes == 4) {
+                const float4 f = __ldcs(reinterpret_cast<const float4*>(static_cast<const Tp*>(a.V_new) + at) + lane);
+                v[0] = f.x;
+                v[1] = f.y;
+                v[2] = f.z;
+                v[3] = f.w;
+            } else {
+                const uint2 f = __ldcs(reinterpret_cast<const uint2*>(static_cast<const Tp*>(a.V_new) + at) + lane);
+                v[0] = bf16_lo(f.x);
+                v[1] = bf16_hi(f.x);
+                v[2] = bf16_lo(f.y);
+                v[3] = bf16_hi(f.y);
+            }
+        }
         const ApSeq sq = append_seq(a, b, t == 0 && lane == 0 && hk == 0);
         j = sq.p0 + t;
         first = sq.lo;
         live = j >= sq.lo && j < sq.hi;
-        const int64_t at = (((int64_t)b * a.H_kv + hk) * a.T + t) * D;
         if (live) {
-            if (lane < D >> 4) {
-                const bool turn = a.rope != nullptr && lane < a.rot_dim >> 4;
-                int ca, cb;
-                unit_cols(turn ? a.rot_dim : 0, a.interleaved, lane, &ca, &cb);
-                Chunk<E> wa, wb;
-                wa.load(static_cast<const Tp*>(a.K_new) + at + ca);
-                wb.load(static_cast<const Tp*>(a.K_new) + at + cb);
+            row = pool_row(a, b, hk, (int)j);
+            if (unit_on) {
                 float x[16];
                 wa.get(x);
                 wb.get(x + 8);
@@ -397,22 +416,6 @@ __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) 
                 for (int e = 0; e < 8; ++e) {
                     xs[warp][ca + e] = x[e];
                     xs[warp][cb + e] = x[8 + e];
-                }
-            }
-            row = pool_row(a, b, hk, (int)j);
-            if (lane_on) {
-                if constexpr (E::kBytes == 4) {
-                    const float4 f = __ldcs(reinterpret_cast<const float4*>(static_cast<const Tp*>(a.V_new) + at) + lane);
-                    v[0] = f.x;
-                    v[1] = f.y;
-                    v[2] = f.z;
-                    v[3] = f.w;
-                } else {
-                    const uint2 f = __ldcs(reinterpret_cast<const uint2*>(static_cast<const Tp*>(a.V_new) + at) + lane);
-                    v[0] = bf16_lo(f.x);
-                    v[1] = bf16_hi(f.x);
-                    v[2] = bf16_lo(f.y);
-                    v[3] = bf16_hi(f.y);
                 }
             }
         }
@@ -581,13 +584,12 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
     cudaError_t e = dev_info(&di);
     if (e != cudaSuccess) return e;
     if (a.T <= kRwRows) {
-        // sequences of a CTA: as many as still leave a CTA for every SM
-        int64_t group = (int64_t)a.B * a.H_kv / di.sm_count;
-        group = group < 1 ? 1 : group;
-        group = min64(min64(group, kRwRows / a.T), a.B);
-        a.group = (int)group;
-        const int64_t kv = (a.B + group - 1) / group * a.H_kv;
+        // sequences of a CTA: the fewest with which the CTAs are resident together (one to an SM)
         const int64_t q = a.q != nullptr ? ((int64_t)a.B * a.H_q * a.T * 8 + kRwThreads - 1) / kRwThreads : 0;
+        int64_t group = 1, kv = (int64_t)a.B * a.H_kv;
+        while (kv + q > di.sm_count && group < a.B && (group + 1) * a.T <= kRwRows)
+            kv = (a.B + group) / (group + 1) * a.H_kv, ++group;
+        a.group = (int)group;
         if (kv + q > 0x7fffffff) return cudaErrorInvalidValue;
         a.kv_ctas = (int)kv;
         return a.D == 96 ? rows_impl<E, kQ8, 96>(a, kv + q, s) : rows_impl<E, kQ8, 128>(a, kv + q, s);
