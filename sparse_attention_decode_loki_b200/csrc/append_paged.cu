@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
 // basis column sits in each thread's registers, loaded before anything else;
 // a warp per row turns it, quantises it and stores it.
 
-constexpr int kRwThreads = 512, kRwRows = 16;
+constexpr int kRwThreads = 512, kRwRows = kRwThreads / 32;  // a row to a warp
 
 template <class E, bool kQ8, int D, bool kBasis>
 __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) {

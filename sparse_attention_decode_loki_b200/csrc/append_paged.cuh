@@ -19,7 +19,8 @@
 
 namespace loki {
 
-// The appended tokens of sequence b that get written: positions [lo, hi).
+// The appended tokens of sequence b that get written: positions [lo, hi), or
+// lo = hi = 0.
 // Tokens outside the block table or behind the rope table are left out, and
 // flagged when `flag`.
 struct ApSeq {
@@ -41,6 +42,7 @@ __device__ __forceinline__ ApSeq append_seq(const AppendArgs& a, int b, bool fla
     }
     if (a.rope != nullptr && a.n_pos < lim) lim = a.n_pos;
     s.hi = s.hi < lim ? s.hi : lim;
+    if (s.hi <= s.lo) s.lo = s.hi = 0;  // no token: no run and no scale block is touched
     return s;
 }
 

@@ -124,6 +124,27 @@ def test_python_wants_cuda_tensors_and_types():
         loki.loki_append_keys_paged_rope(q[None], q[None], None, q[None], q[None], bt, sl)
 
 
+def test_binding_refuses_what_is_no_tensor_or_number():
+    torch = pytest.importorskip("torch")
+    from sparse_attention_decode_loki_b200 import _binding as b
+    with pytest.raises(ValueError):
+        b.place(torch.zeros(2))
+    with pytest.raises(TypeError):
+        b.place(3)
+    assert b.place(None) == -1
+    with pytest.raises(TypeError):
+        b.loki_rope_table(None, 8, 64)
+    with pytest.raises(TypeError):
+        b.loki_rope_table("x", 8, 64, 10000.0, 1.0, None)
+    with pytest.raises(TypeError):
+        b.loki_rope_table(F, 8.5, 64, 10000.0, 1.0, None)
+    with pytest.raises(OverflowError):
+        b.loki_rope_table(F, 8, 1 << 40, 10000.0, 1.0, None)
+    assert b.loki_rope_table(None, 8, 64, 10000.0, 1.0, None) == 1  # the C entry's own refusals
+    with pytest.raises(TypeError):
+        b.empty_like(3)
+
+
 # --- the restatement's own pins -------------------------------------------------
 
 def test_e4m3_rounding_agrees_with_the_type():
