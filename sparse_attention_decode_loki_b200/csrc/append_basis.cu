@@ -6,7 +6,7 @@
 // as fp32 would give it (the plane's scores choose tokens by it). Both sides
 // are carried as two fp16 parts, x = hi + lo (22 bits, after a power of two
 // per row of keys and per column of P has brought the largest entry to
-// 2^14..2^15), and three of the four products are taken: hi hi, hi lo, lo hi;
+// 2^14..2^15), and three of the four products are taken: lo hi, hi lo, hi hi;
 // the fourth lies below 2^-22 of the product. So 6 D flop per output, at the
 // fp16 rate with fp32 accumulators in tensor memory.
 //
@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t at = (k >> 2) * kAbAtom + (k & 3) * 32;
-                        mma_f16_ss(tmem, smem_desc(sa + (pass == 2 ? 2 * kAbAtom : 0) + at),
+                        // lo hi, hi lo, then hi hi: the accumulator truncates at every step, so the small
+                        // products come while it is small
+                        mma_f16_ss(tmem, smem_desc(sa + (pass == 0 ? 2 * kAbAtom : 0) + at),
                                    smem_desc(sb + (pass == 1 ? 2 * kAbAtom : 0) + at), idesc, pass + k > 0);
                     }
                 asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
