@@ -398,22 +398,24 @@ def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rop
     """What the two rotary appends share: (device index, H_q, q_out, the C arguments around the pages)."""
     i = _b.place(K_new, V_new, K_pages, V_pages, block_table, positions, P, rope_table, plane,
                  new_lens, q, q_out, *scales)
-    ks, ps, bs, dtype = K_new.shape, K_pages.shape, block_table.shape, K_new.dtype
-    if len(ks) != 4 or len(ps) != 4 or len(bs) != 2:
+    ks, ps, dtype = K_new.shape, K_pages.shape, K_new.dtype
+    if len(ks) != 4 or len(ps) != 4 or block_table.dim() != 2:
         raise ValueError("K_new [B, H_kv, T, D], pages [n_pages, H_kv, page_size, D] and "
                          "block_table [B, max_pages] expected")
     B, H_kv, T, D = ks
     n_pages, Hp, page_size, Dp = ps
-    if (V_new.shape != ks or V_pages.shape != ps or Hp != H_kv or Dp != D or bs[0] != B
-            or positions.shape != (B,)):
+    max_pages = block_table.shape[1]
+    dt, fits = _dt(K_new), _b.fits
+    if not (fits(V_new, dtype, B, H_kv, T, D) and Hp == H_kv and Dp == D
+            and fits(V_pages, K_pages.dtype, n_pages, H_kv, page_size, D)
+            and fits(block_table, torch.int32, B, max_pages) and fits(positions, torch.int32, B)):
+        if block_table.dtype != torch.int32 or positions.dtype != torch.int32:
+            raise TypeError("block_table and positions must be int32")
+        if V_new.dtype != dtype or V_pages.dtype != K_pages.dtype:
+            raise TypeError("K_new and V_new, and the two page pools, must share a dtype")
         raise ValueError("K_new, V_new [B, H_kv, T, D], the pages, block_table [B, max_pages] and "
                          "positions [B] disagree")
-    if block_table.dtype != torch.int32 or positions.dtype != torch.int32:
-        raise TypeError("block_table and positions must be int32")
-    dt = _dt(K_new)
-    if V_new.dtype != dtype or V_pages.dtype != K_pages.dtype:
-        raise TypeError("K_new and V_new, and the two page pools, must share a dtype")
-    if P is not None:
+    if P is not None and not fits(P, torch.float32, H_kv, D, D):
         _expect(P, (H_kv, D, D), torch.float32, "P")
     table = (None, 0, 0)
     if rope_table is not None:
@@ -425,23 +427,25 @@ def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rop
         if plane.dim() != 4:
             raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
         d_lo = plane.shape[3]
-        _expect(plane, (n_pages, H_kv, page_size, d_lo), dtype, "Kt_lo_pages")
-    if new_lens is not None:
+        if not fits(plane, dtype, n_pages, H_kv, page_size, d_lo):
+            _expect(plane, (n_pages, H_kv, page_size, d_lo), dtype, "Kt_lo_pages")
+    if new_lens is not None and not fits(new_lens, torch.int32, B):
         _expect(new_lens, (B,), torch.int32, "new_lens")
     H_q = H_kv
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be [B, H_q, T, D]")
         H_q = q.shape[1]
-        _expect(q, (B, H_q, T, D), dtype, "q")
+        if not fits(q, dtype, B, H_q, T, D):
+            _expect(q, (B, H_q, T, D), dtype, "q")
         if q_out is None:
             q_out = _b.empty_like(q)
-        else:
+        elif not fits(q_out, dtype, B, H_q, T, D):
             _expect(q_out, q.shape, q.dtype, "q_out")
     elif q_out is not None:
         raise ValueError("q_out needs q")
     return (i, H_q, q_out, (K_new, V_new, P, *table),
-            (plane, d_lo, block_table, positions, new_lens, B, H_kv, T, page_size, bs[1], n_pages, D, dt))
+            (plane, d_lo, block_table, positions, new_lens, B, H_kv, T, page_size, max_pages, n_pages, D, dt))
 
 
 def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
@@ -468,18 +472,21 @@ def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Opt
 
 def _check_q8(K8_pages, V8_pages, k_scales, v_scales):
     """(block) of 8-bit pages and their scales."""
-    if K8_pages.dtype != torch.float8_e4m3fn or V8_pages.dtype != torch.float8_e4m3fn:
+    f8 = torch.float8_e4m3fn
+    if K8_pages.dtype != f8 or V8_pages.dtype != f8:
         raise TypeError("8-bit pages must be torch.float8_e4m3fn")
-    ps, ss = K8_pages.shape, k_scales.shape
-    if len(ps) != 4 or V8_pages.shape != ps or len(ss) != 3:
+    ps = K8_pages.shape
+    if len(ps) != 4 or not _b.fits(V8_pages, f8, *ps) or k_scales.dim() != 3:
         raise ValueError("pages [n_pages, H_kv, page_size, D] and scales [n_pages, H_kv, "
                          "page_size / block] expected")
     n_pages, H_kv, page_size, _ = ps
-    nb = ss[2]
+    nb = k_scales.shape[2]
     if nb < 1 or page_size % nb:
         raise ValueError("page_size must be a multiple of the scales' blocks per page")
-    _expect(k_scales, (n_pages, H_kv, nb), torch.float32, "k_scales")
-    _expect(v_scales, (n_pages, H_kv, nb), torch.float32, "v_scales")
+    if not (_b.fits(k_scales, torch.float32, n_pages, H_kv, nb)
+            and _b.fits(v_scales, torch.float32, n_pages, H_kv, nb)):
+        _expect(k_scales, (n_pages, H_kv, nb), torch.float32, "k_scales")
+        _expect(v_scales, (n_pages, H_kv, nb), torch.float32, "v_scales")
     return page_size // nb
 
 
@@ -524,15 +531,16 @@ def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq
     block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
     i = _b.place(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, *more)
     n_pages, H_kv, page_size, D = K8_pages.shape
-    qs, bs = q.shape, block_table.shape
-    if len(qs) != 3 or len(bs) != 2:
+    qs = q.shape
+    if len(qs) != 3 or block_table.dim() != 2:
         raise ValueError("q [B, H_q, D] and block_table [B, max_pages] expected")
     B, H_q, Dq = qs
-    if Dq != D or bs[0] != B or seq_lens.shape != (B,):
+    max_pages = block_table.shape[1]
+    if not (Dq == D and _b.fits(block_table, torch.int32, B, max_pages) and _b.fits(seq_lens, torch.int32, B)):
+        if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+            raise TypeError("block_table and seq_lens must be int32")
         raise ValueError("q [B, H_q, D], block_table [B, max_pages], seq_lens [B] disagree")
-    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_table and seq_lens must be int32")
-    return i, (B, H_q, H_kv, page_size, bs[1], n_pages, D), (q, K8_pages, V8_pages, k_scales, v_scales, block)
+    return i, (B, H_q, H_kv, page_size, max_pages, n_pages, D), (q, K8_pages, V8_pages, k_scales, v_scales, block)
 
 
 _dense_q8_ws = functools.lru_cache(maxsize=1024)(dense_decode_paged_q8_workspace_size)

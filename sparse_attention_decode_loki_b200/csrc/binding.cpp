@@ -92,6 +92,22 @@ PyObject* place(PyObject*, PyObject* const* args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// fits(t, dtype, d0, d1, ...): whether t is a tensor of this type and shape
+PyObject* fits(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n < 2 || !THPVariable_Check(args[0]) || !THPDtype_Check(args[1]))
+        return PyErr_Format(PyExc_TypeError, "fits(tensor, dtype, *shape)");
+    const at::Tensor& t = THPVariable_Unpack(args[0]);
+    bool ok = t.scalar_type() == reinterpret_cast<THPDtype*>(args[1])->scalar_type && t.dim() == n - 2;
+    for (Py_ssize_t i = 2; ok && i < n; ++i) {
+        const long long d = PyLong_AsLongLong(args[i]);
+        if (d == -1 && PyErr_Occurred()) return nullptr;
+        ok = t.size(i - 2) == d;
+    }
+    return PyBool_FromLong(ok);
+    END_HANDLE_TH_ERRORS
+}
+
 // scratch(like, nbytes): uninitialised bytes on like's device
 PyObject* scratch(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -118,6 +134,7 @@ PyObject* empty_like(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define LOKI_CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&Call<&f>::run)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"place", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&place)), METH_FASTCALL, nullptr},
+    {"fits", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&fits)), METH_FASTCALL, nullptr},
     {"scratch", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&scratch)), METH_FASTCALL, nullptr},
     {"empty_like", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&empty_like)), METH_FASTCALL, nullptr},
     LOKI_CALL(loki_rope_table),
