@@ -22,6 +22,13 @@
 // holds one row: stored directly, each 16 bytes would touch another line, which
 // took 1.5 us a tile). Rows that hold an infinity or a NaN take the plain fp32
 // sum instead (an infinity has no second part).
+//
+// Measured on a 4096-token prompt of 32 heads into 8 bits: 53 us alone, 65 us
+// with the stream (27 alone) beside it; 7 us a tile, of which 1.7 us turn and
+// split, 1.2 us products, 1.6 us the two passes over the product, 0.7 us copies.
+// Latencies of these phases bound it (36 % of issue slots, 13 % of the tensor
+// pipe). Two groups of warps with an A each took the whole SM and 55 us; a warp
+// of its own for the products caps 17 warps at 96 registers, which spill: 69.
 #include <cuda_fp16.h>
 
 #include "append_paged.cuh"

@@ -9,16 +9,22 @@ namespace loki {
 // ---------------------------------------------------------------------------
 // Longer appends as streams, one read and one write of each row. Bytes bound
 // them, and what the loads in flight cost is registers: values and queries
-// share a kernel of up to 24 warps an SM; keys without a basis, which are turned
-// and then scaled, have one of their own, a CTA to an SM, which runs beside it.
+// share a kernel of 64 registers, 32 warps an SM; keys without a basis, which
+// are turned and then scaled, have one of their own, a CTA to an SM, which runs
+// beside it.
 //
 // Values and keys: a CTA has an aligned run of 128 positions and goes through
 // some heads, a warp has 16 of the positions, eight lanes to a row (16 columns
-// each); the next head's rows are loaded before this one's are stored. 8-bit scale blocks of more than 16 tokens belong to neighbouring
-// warps, which share their largest magnitude through shared memory, so every
-// scale has one owner.
+// each); the next head's rows are loaded before this one's are stored. 8-bit
+// scale blocks of more than 16 tokens belong to neighbouring warps, which share
+// their largest magnitude through shared memory, so every scale has one owner.
 // Queries: a warp has four positions, whose angles stay in its registers while
 // it goes through the heads.
+//
+// Measured on two prompts of 8192 and 6144 tokens, 32 query and 8 KV heads, into
+// 8 bits: 55 us for values and queries (279 MB, 5.1 TB/s), 35 us for keys, 77 us
+// side by side. Rows of all heads in one 16-row warp item with the angles in
+// shared memory took 103 us, U = 3 or 4 heads in flight 84 to 86.
 
 constexpr int kStThreads = 256, kStQueryRows = 32;
 
@@ -320,7 +326,9 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
 // Few tokens (a decode step), with or without a basis. Latency bounds it: one
 // CTA per KV head and group of sequences, at most 16 rows. A quarter of a
 // basis column sits in each thread's registers, loaded before anything else;
-// a warp per row turns it, quantises it and stores it.
+// a warp per row turns it, quantises it and stores it. 16 sequences of 40 heads:
+// 4.4 us (8 bits 5.2); in two waves of CTAs it took 8.0 (9.3), in two CTAs an SM
+// of 64 registers 6.2 (7.1).
 
 constexpr int kRwThreads = 512, kRwRows = kRwThreads / 32;  // a row to a warp
 

@@ -37,18 +37,24 @@
 // page, come as two bulk copies; selected tokens as cp.async, every lane
 // fetching and reading back its own fragments.
 //
-// The tiles of all (sequence, KV head) units - of all (sequence, query head)
-// rows, when tokens are selected - are laid end to end and dealt to warps in
-// runs: four fifths of the line to the warps that are resident together, the
-// last fifth in runs a quarter as long to as many warps behind them, which
-// the SMs that are done first take up (SMs differ by 15 % in what the memory
-// gives them; equal runs left the others idle for a fifth of the time).
-// Which warp reduces which tiles is fixed all the same. A warp that owns a
-// whole unit writes its output, others leave partials (fp32 max, sum, D
-// columns per head) that k_q8_combine merges in a fixed order. Where that would leave a warp only a
-// few tiles, latency counts, and one kernel does it all: a cluster of CTAs
-// takes a unit, its warps a run of tiles each, and the partials meet in
-// shared memory, the CTAs' through distributed shared memory.
+// Work is dealt in one of two ways (cluster_size chooses). A cluster of CTAs
+// takes a unit - a (sequence, KV head), or a (sequence, query head) row when
+// tokens are selected - its warps a run of tiles each, and the partials meet in
+// shared memory, the CTAs' through distributed shared memory: one kernel. Where
+// whole units would leave much of the device empty, the tiles of all units are
+// laid end to end and dealt to warps in runs: four fifths of the line to the
+// warps that are resident together, the last fifth in runs a quarter as long to
+// as many warps behind them, which the SMs that are done first take up (SMs
+// differ by 15 % in what the memory gives them; equal runs left the others idle
+// for a fifth of the time). A warp that owns a whole unit writes its output,
+// others leave partials (fp32 max, sum, D columns per head) that k_q8_combine
+// merges. Either way which warp reduces which tiles is fixed by sizes alone.
+//
+// Measured, inputs in DRAM: 16 ragged sequences to 4096 tokens, 40 heads, 436 MB
+// in 69 to 76 us (6.0 TB/s; 69 without any arithmetic in the two-kernel form);
+// 4 x 32768 tokens, 8 KV heads for 32, 218 MB in 43 us; 512 selected tokens for
+// each of 640 rows, 79 MB of random 128-byte rows in 25 us (21 without
+// arithmetic); one sequence of 513 tokens, 32 heads, 7.2 us.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
