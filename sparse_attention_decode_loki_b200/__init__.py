@@ -543,6 +543,18 @@ def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq
     return i, (B, H_q, H_kv, page_size, max_pages, n_pages, D), (q, K8_pages, V8_pages, k_scales, v_scales, block)
 
 
+_SPARE = {}  # device index -> the workspace of calls that leave it alone
+
+
+def _q8_ws(like: torch.Tensor, i: int, nbytes: int) -> torch.Tensor:
+    """A workspace of nbytes; where the call needs none (the least size), one that all such calls share."""
+    if nbytes > 256:
+        return _b.scratch(like, nbytes)
+    if i not in _SPARE:
+        _SPARE[i] = _b.scratch(like, 256)
+    return _SPARE[i]
+
+
 _dense_q8_ws = functools.lru_cache(maxsize=1024)(dense_decode_paged_q8_workspace_size)
 _sparse_q8_ws = functools.lru_cache(maxsize=1024)(loki_sparse_attention_paged_q8_workspace_size)
 _decode_q8_ws = functools.lru_cache(maxsize=1024)(loki_paged_q8_decode_workspace_size)
@@ -565,7 +577,7 @@ def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
         _expect(out, q.shape, q.dtype, "out")
     ws = workspace
     if ws is None:
-        ws = _b.scratch(q, _dense_q8_ws(B, H_q, H_kv, page_size, max_pages, D))
+        ws = _q8_ws(q, i, _dense_q8_ws(B, H_q, H_kv, page_size, max_pages, D))
     _launch(_b.dense_decode_attention_paged_q8, "dense_decode_attention_paged_q8", i, *front,
             block_table, seq_lens, *sizes, scale, _dt(q), out, ws, ws.nbytes)
     return out
@@ -595,7 +607,7 @@ def loki_sparse_attention_paged_q8(q_rot: torch.Tensor, K8_pages: torch.Tensor,
         _expect(out, (B, H_q, D), out.dtype, "out")
     ws = workspace
     if ws is None:
-        ws = _b.scratch(q_rot, _sparse_q8_ws(B, H_q, H_kv, k, D))
+        ws = _q8_ws(q_rot, i, _sparse_q8_ws(B, H_q, H_kv, k, D))
     _launch(_b.loki_sparse_attention_paged_q8, "loki_sparse_attention_paged_q8", i, *front,
             block_table, seq_lens, selected_idx, *sizes, k, scale, _dt(out), out, ws, ws.nbytes)
     return out

@@ -76,7 +76,7 @@ namespace cg = cooperative_groups;
 constexpr int kQ8Threads = 128;
 constexpr int kClThreads = 256;  // of the cluster kernels
 constexpr int kStages = 3;
-constexpr int kClusterTiles = 10;  // tiles for every resident warp up to which the clusters may be few
+constexpr int kClusterTiles = 23680;  // up to so many tiles (ten for every resident warp) clusters may be few
 constexpr int kQ8MaxWarps = 2 * 148 * 16;  // workspace is laid out for at most this many
 constexpr int kTile = 16;
 constexpr uint32_t kNoRow = 0xffffffffu;
@@ -870,7 +870,9 @@ static int64_t q8_slots(int64_t units, int64_t tiles) {
     return (units + min64(kQ8MaxWarps, 2 * tiles) + 1) & ~(int64_t)1;
 }
 
+// (none where clusters are sure: the calls still want a workspace, of any size)
 static size_t q8_ws_bytes(int64_t units, int64_t tiles, int G, int D) {
+    if (tiles <= kClusterTiles) return 1;
     return (size_t)q8_slots(units, tiles) * G * (sizeof(float2) + D * sizeof(float));
 }
 
@@ -943,21 +945,29 @@ static cudaError_t cluster_slots(const void* kern, size_t smem, ClusterSlots* ou
 //   8 x 2 x 65536 (43 % of the places filled) 67 / 55, 40 x 8 x 4096 (54 %)
 //   75 / 63, 8 x 1 x 131072 (22 %) 114 / 75; 8 x 1 x 32768 (22 %, but few
 //   tiles) 32 / 38.
+// Sizes: meeting the other CTAs costs about a tile's time, so two tiles a warp
+// stay in one CTA (32 units of 16 tiles 5.7 us, in clusters of 2 to 8 6.1) and
+// 64 tiles in four (7.2; in eight 7.6); sizes other than powers of two lose 15 %
+// at the same number of tiles a warp (33 tiles: 4 CTAs 7.1, 5 CTAs 7.4; 128: 4
+// CTAs 8.9, 5 CTAs 10.8) but fill more (80 units of 1024 tiles: 2 CTAs 65, 3 51).
 static int cluster_size(int64_t units, int64_t tiles, const ClusterSlots& slots) {
     constexpr int W = kClThreads / 32;
     const int64_t resident = slots.active[1];
     int best = 1;
-    double fill = 0;
-    for (int c = 1; c <= 8 && (c == 1 || (c - 1) * W < tiles); ++c) {
-        if (slots.active[c] < 1 || (c > 1 && units > slots.active[c])) continue;
+    double fill = 0, most = 0;
+    for (int c = 1; c <= 8; ++c) {
+        const bool useful = c == 1 || (tiles > 2 * W && (c - 1) * W < tiles && (c <= 4 || tiles > 8 * W));
+        if (!useful || slots.active[c] < 1 || (c > 1 && units > slots.active[c])) continue;
         const int64_t waves = (units + slots.active[c] - 1) / slots.active[c];
         const double f = (double)(units * c) / (double)(waves * resident);
-        if (f >= fill) {
+        const double worth = (c & (c - 1)) == 0 ? f : 0.8 * f;
+        if (worth >= most) {
+            most = worth;
             fill = f;
             best = c;
         }
     }
-    return fill >= 0.7 || units * tiles <= kClusterTiles * W * resident ? best : 0;
+    return fill >= 0.7 || units * tiles <= kClusterTiles ? best : 0;
 }
 
 // the pages as a [rows, 128] byte matrix, in boxes of one tile
