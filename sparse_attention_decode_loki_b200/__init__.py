@@ -13,7 +13,6 @@ top k are kept, and exact softmax attention runs over those k tokens only.
 """
 from __future__ import annotations
 
-import functools
 from typing import Optional, Tuple
 
 import torch
@@ -368,17 +367,6 @@ def loki_append_keys_paged(K_new: torch.Tensor, V_new: torch.Tensor, P: torch.Te
 # paged appends with the rotary embedding, 8-bit pages
 # ---------------------------------------------------------------------------
 
-def _launch(f, name: str, i: int, *args) -> None:
-    """Calls the library's entry on device i's current stream, with i as the current device."""
-    if torch.cuda.current_device() == i:
-        status = f(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(i):
-            status = f(*args, _raw_stream(i))
-    if status != 0:
-        check(status, name)
-
-
 def loki_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, pos_scale: float = 1.0,
                     device: Optional[torch.device] = None,
                     table: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -387,65 +375,10 @@ def loki_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, pos_scale: 
     if table is None:
         table = torch.empty((n_pos, rot_dim), dtype=torch.float32,
                             device="cuda" if device is None else device)
-    i = _b.place(table)
+    _cuda(table)
     _expect(table, (n_pos, rot_dim), torch.float32, "table")
-    _launch(_b.loki_rope_table, "loki_rope_table", i, table, n_pos, rot_dim, base, pos_scale)
+    check(_b.rope_table(table, base, pos_scale)[0], "loki_rope_table")
     return table
-
-
-def _check_append(K_new, V_new, P, K_pages, V_pages, block_table, positions, rope_table, plane,
-                  new_lens, q, q_out, *scales):
-    """What the two rotary appends share: (device index, H_q, q_out, the C arguments around the pages)."""
-    i = _b.place(K_new, V_new, K_pages, V_pages, block_table, positions, P, rope_table, plane,
-                 new_lens, q, q_out, *scales)
-    ks, ps, dtype = K_new.shape, K_pages.shape, K_new.dtype
-    if len(ks) != 4 or len(ps) != 4 or block_table.dim() != 2:
-        raise ValueError("K_new [B, H_kv, T, D], pages [n_pages, H_kv, page_size, D] and "
-                         "block_table [B, max_pages] expected")
-    B, H_kv, T, D = ks
-    n_pages, Hp, page_size, Dp = ps
-    max_pages = block_table.shape[1]
-    dt, fits = _dt(K_new), _b.fits
-    if not (fits(V_new, dtype, B, H_kv, T, D) and Hp == H_kv and Dp == D
-            and fits(V_pages, K_pages.dtype, n_pages, H_kv, page_size, D)
-            and fits(block_table, torch.int32, B, max_pages) and fits(positions, torch.int32, B)):
-        if block_table.dtype != torch.int32 or positions.dtype != torch.int32:
-            raise TypeError("block_table and positions must be int32")
-        if V_new.dtype != dtype or V_pages.dtype != K_pages.dtype:
-            raise TypeError("K_new and V_new, and the two page pools, must share a dtype")
-        raise ValueError("K_new, V_new [B, H_kv, T, D], the pages, block_table [B, max_pages] and "
-                         "positions [B] disagree")
-    if P is not None and not fits(P, torch.float32, H_kv, D, D):
-        _expect(P, (H_kv, D, D), torch.float32, "P")
-    table = (None, 0, 0)
-    if rope_table is not None:
-        if rope_table.dim() != 2 or rope_table.dtype != torch.float32:
-            raise ValueError("rope_table must be float32 [n_pos, rot_dim]")
-        table = (rope_table, *rope_table.shape)
-    d_lo = 0
-    if plane is not None:
-        if plane.dim() != 4:
-            raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
-        d_lo = plane.shape[3]
-        if not fits(plane, dtype, n_pages, H_kv, page_size, d_lo):
-            _expect(plane, (n_pages, H_kv, page_size, d_lo), dtype, "Kt_lo_pages")
-    if new_lens is not None and not fits(new_lens, torch.int32, B):
-        _expect(new_lens, (B,), torch.int32, "new_lens")
-    H_q = H_kv
-    if q is not None:
-        if q.dim() != 4:
-            raise ValueError("q must be [B, H_q, T, D]")
-        H_q = q.shape[1]
-        if not fits(q, dtype, B, H_q, T, D):
-            _expect(q, (B, H_q, T, D), dtype, "q")
-        if q_out is None:
-            q_out = _b.empty_like(q)
-        elif not fits(q_out, dtype, B, H_q, T, D):
-            _expect(q_out, q.shape, q.dtype, "q_out")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    return (i, H_q, q_out, (K_new, V_new, P, *table),
-            (plane, d_lo, block_table, positions, new_lens, B, H_kv, T, page_size, max_pages, n_pages, D, dt))
 
 
 def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
@@ -461,33 +394,11 @@ def loki_append_keys_paged_rope(K_new: torch.Tensor, V_new: torch.Tensor, P: Opt
     and turn the queries q [B, H_q, T, D] by the same angles; returns q_out (None without q).
     P None: no basis; rope_table None: no rotary embedding; new_lens [B] int32: only the first
     new_lens[b] tokens (see include/loki.h)."""
-    i, H_q, q_out, front, back = _check_append(K_new, V_new, P, Kt_pages, V_pages, block_table,
-                                               positions, rope_table, Kt_lo_pages, new_lens, q, q_out)
-    if Kt_pages.dtype != K_new.dtype:
-        raise TypeError("K_new and the pages must share a dtype")
-    _launch(_b.loki_append_keys_paged_rope, "loki_append_keys_paged_rope", i, *front,
-            bool(interleaved), q, q_out, H_q, Kt_pages, V_pages, *back)
+    status, q_out = _b.append(K_new, V_new, P, Kt_pages, V_pages, None, None, block_table, positions,
+                              rope_table, interleaved, Kt_lo_pages, new_lens, q, q_out)
+    if status:
+        check(status, "loki_append_keys_paged_rope")
     return q_out
-
-
-def _check_q8(K8_pages, V8_pages, k_scales, v_scales):
-    """(block) of 8-bit pages and their scales."""
-    f8 = torch.float8_e4m3fn
-    if K8_pages.dtype != f8 or V8_pages.dtype != f8:
-        raise TypeError("8-bit pages must be torch.float8_e4m3fn")
-    ps = K8_pages.shape
-    if len(ps) != 4 or not _b.fits(V8_pages, f8, *ps) or k_scales.dim() != 3:
-        raise ValueError("pages [n_pages, H_kv, page_size, D] and scales [n_pages, H_kv, "
-                         "page_size / block] expected")
-    n_pages, H_kv, page_size, _ = ps
-    nb = k_scales.shape[2]
-    if nb < 1 or page_size % nb:
-        raise ValueError("page_size must be a multiple of the scales' blocks per page")
-    if not (_b.fits(k_scales, torch.float32, n_pages, H_kv, nb)
-            and _b.fits(v_scales, torch.float32, n_pages, H_kv, nb)):
-        _expect(k_scales, (n_pages, H_kv, nb), torch.float32, "k_scales")
-        _expect(v_scales, (n_pages, H_kv, nb), torch.float32, "v_scales")
-    return page_size // nb
 
 
 def loki_append_keys_paged_q8(K_new: torch.Tensor, V_new: torch.Tensor, P: Optional[torch.Tensor],
@@ -501,12 +412,10 @@ def loki_append_keys_paged_q8(K_new: torch.Tensor, V_new: torch.Tensor, P: Optio
                               q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """loki_append_keys_paged_rope into 8-bit pages: e4m3 codes [n_pages, H_kv, page_size, D]
     (torch.float8_e4m3fn) with fp32 scales [n_pages, H_kv, page_size / block], powers of two."""
-    block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
-    i, H_q, q_out, front, back = _check_append(K_new, V_new, P, K8_pages, V8_pages, block_table,
-                                               positions, rope_table, Kt_lo_pages, new_lens, q, q_out,
-                                               k_scales, v_scales)
-    _launch(_b.loki_append_keys_paged_q8, "loki_append_keys_paged_q8", i, *front, bool(interleaved),
-            q, q_out, H_q, K8_pages, V8_pages, k_scales, v_scales, block, *back)
+    status, q_out = _b.append(K_new, V_new, P, K8_pages, V8_pages, k_scales, v_scales, block_table,
+                              positions, rope_table, interleaved, Kt_lo_pages, new_lens, q, q_out)
+    if status:
+        check(status, "loki_append_keys_paged_q8")
     return q_out
 
 
@@ -525,41 +434,6 @@ def loki_paged_q8_decode_workspace_size(B: int, H_q: int, H_kv: int, page_size: 
     return int(lib.loki_paged_q8_decode_workspace_size(B, H_q, H_kv, page_size, max_pages, D, d, k))
 
 
-def _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, *more):
-    """What the attentions over 8-bit pages share: (device index, the sizes B, H_q, H_kv, page_size,
-    max_pages, n_pages, D of the C calls, the C arguments in front of their own)."""
-    block = _check_q8(K8_pages, V8_pages, k_scales, v_scales)
-    i = _b.place(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, *more)
-    n_pages, H_kv, page_size, D = K8_pages.shape
-    qs = q.shape
-    if len(qs) != 3 or block_table.dim() != 2:
-        raise ValueError("q [B, H_q, D] and block_table [B, max_pages] expected")
-    B, H_q, Dq = qs
-    max_pages = block_table.shape[1]
-    if not (Dq == D and _b.fits(block_table, torch.int32, B, max_pages) and _b.fits(seq_lens, torch.int32, B)):
-        if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-            raise TypeError("block_table and seq_lens must be int32")
-        raise ValueError("q [B, H_q, D], block_table [B, max_pages], seq_lens [B] disagree")
-    return i, (B, H_q, H_kv, page_size, max_pages, n_pages, D), (q, K8_pages, V8_pages, k_scales, v_scales, block)
-
-
-_SPARE = {}  # device index -> the workspace of calls that leave it alone
-
-
-def _q8_ws(like: torch.Tensor, i: int, nbytes: int) -> torch.Tensor:
-    """A workspace of nbytes; where the call needs none (the least size), one that all such calls share."""
-    if nbytes > 256:
-        return _b.scratch(like, nbytes)
-    if i not in _SPARE:
-        _SPARE[i] = _b.scratch(like, 256)
-    return _SPARE[i]
-
-
-_dense_q8_ws = functools.lru_cache(maxsize=1024)(dense_decode_paged_q8_workspace_size)
-_sparse_q8_ws = functools.lru_cache(maxsize=1024)(loki_sparse_attention_paged_q8_workspace_size)
-_decode_q8_ws = functools.lru_cache(maxsize=1024)(loki_paged_q8_decode_workspace_size)
-
-
 def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
                                     V8_pages: torch.Tensor, k_scales: torch.Tensor,
                                     v_scales: torch.Tensor, block_table: torch.Tensor,
@@ -568,18 +442,10 @@ def dense_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor,
                                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Full attention of q [B, H_q, D] over each sequence's seq_lens[b] tokens in 8-bit pages
     (see include/loki.h). Returns out [B, H_q, D] of q's dtype."""
-    i, sizes, front = _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table,
-                                       seq_lens, out, workspace)
-    B, H_q, H_kv, page_size, max_pages, _, D = sizes
-    if out is None:
-        out = _b.empty_like(q)
-    else:
-        _expect(out, q.shape, q.dtype, "out")
-    ws = workspace
-    if ws is None:
-        ws = _q8_ws(q, i, _dense_q8_ws(B, H_q, H_kv, page_size, max_pages, D))
-    _launch(_b.dense_decode_attention_paged_q8, "dense_decode_attention_paged_q8", i, *front,
-            block_table, seq_lens, *sizes, scale, _dt(q), out, ws, ws.nbytes)
+    status, out = _b.dense(q, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens, scale, out,
+                           workspace)
+    if status:
+        check(status, "dense_decode_attention_paged_q8")
     return out
 
 
@@ -592,24 +458,10 @@ def loki_sparse_attention_paged_q8(q_rot: torch.Tensor, K8_pages: torch.Tensor,
                                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Exact attention of q_rot [B, H_q, D] fp32 over the tokens selected_idx [B, H_q, k] int32
     names, in 8-bit pages. Returns out [B, H_q, D] of type `dtype` (or out's own)."""
-    i, sizes, front = _check_attend_q8(q_rot, K8_pages, V8_pages, k_scales, v_scales, block_table,
-                                       seq_lens, selected_idx, out, workspace)
-    B, H_q, H_kv, _, _, _, D = sizes
-    if q_rot.dtype != torch.float32:
-        raise TypeError("q_rot must be float32")
-    if selected_idx.dim() != 3:
-        raise ValueError("selected_idx must be [B, H_q, k]")
-    k = selected_idx.shape[2]
-    _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
-    if out is None:
-        out = _b.empty_like(q_rot, dtype)
-    else:
-        _expect(out, (B, H_q, D), out.dtype, "out")
-    ws = workspace
-    if ws is None:
-        ws = _q8_ws(q_rot, i, _sparse_q8_ws(B, H_q, H_kv, k, D))
-    _launch(_b.loki_sparse_attention_paged_q8, "loki_sparse_attention_paged_q8", i, *front,
-            block_table, seq_lens, selected_idx, *sizes, k, scale, _dt(out), out, ws, ws.nbytes)
+    status, out = _b.sparse(q_rot, K8_pages, V8_pages, k_scales, v_scales, block_table, seq_lens,
+                            selected_idx, scale, dtype, out, workspace)
+    if status:
+        check(status, "loki_sparse_attention_paged_q8")
     return out
 
 
@@ -623,26 +475,11 @@ def loki_decode_attention_paged_q8(q: torch.Tensor, K8_pages: torch.Tensor, V8_p
                                    ) -> Tuple[torch.Tensor, torch.Tensor]:
     """loki_decode_attention_paged with keys and values in 8-bit pages (the plane in q's dtype).
     Returns (out [B, H_q, D], selected_idx [B, H_q, k] int32, -1 padded)."""
-    i, sizes, front = _check_attend_q8(q, K8_pages, V8_pages, k_scales, v_scales, block_table,
-                                       seq_lens, Kt_lo_pages, P, out, selected_idx, workspace)
-    B, H_q, H_kv, page_size, max_pages, n_pages, D = sizes
-    if Kt_lo_pages.dim() != 4:
-        raise ValueError("Kt_lo_pages must be [n_pages, H_kv, page_size, d_lo]")
-    d_lo = Kt_lo_pages.shape[3]
-    _expect(Kt_lo_pages, (n_pages, H_kv, page_size, d_lo), q.dtype, "Kt_lo_pages")
-    _expect(P, (H_kv, D, D), torch.float32, "P")
-    if out is None:
-        out = _b.empty_like(q)
-    if selected_idx is None:
-        selected_idx = torch.empty((B, H_q, k), dtype=torch.int32, device=q.device)
-    _expect(out, q.shape, q.dtype, "out")
-    _expect(selected_idx, (B, H_q, k), torch.int32, "selected_idx")
-    ws = workspace
-    if ws is None:
-        ws = _b.scratch(q, _decode_q8_ws(B, H_q, H_kv, page_size, max_pages, D, d, k))
-    _launch(_b.loki_decode_attention_paged_q8, "loki_decode_attention_paged_q8", i, *front,
-            Kt_lo_pages, d_lo, P, block_table, seq_lens, *sizes, d, k, scale, _dt(q), out,
-            selected_idx, ws, ws.nbytes)
+    status, (out, selected_idx) = _b.decode(q, K8_pages, V8_pages, k_scales, v_scales, block_table,
+                                            seq_lens, Kt_lo_pages, P, d, k, scale, out, selected_idx,
+                                            workspace)
+    if status:
+        check(status, "loki_decode_attention_paged_q8")
     return out, selected_idx
 
 

@@ -101,7 +101,7 @@ def build_binding(force: bool = False) -> None:
            "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(shutil.which(_nvcc()) or _nvcc())), "include"),
-           "-L", PKG, "-l:libloki.so", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-L", PKG, "-l:libloki.so", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

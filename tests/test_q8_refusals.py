@@ -126,23 +126,25 @@ def test_python_wants_cuda_tensors_and_types():
 
 def test_binding_refuses_what_is_no_tensor_or_number():
     torch = pytest.importorskip("torch")
+    import sparse_attention_decode_loki_b200 as loki
     from sparse_attention_decode_loki_b200 import _binding as b
-    with pytest.raises(ValueError):
-        b.place(torch.zeros(2))
+    t = torch.zeros(1, 1, 16, 128)
+    p8 = t.to(torch.float8_e4m3fn)
+    sc, bt = torch.ones(1, 1, 1), torch.zeros(1, 1, dtype=torch.int32)
     with pytest.raises(TypeError):
-        b.place(3)
-    assert b.place(None) == -1
-    with pytest.raises(TypeError):
-        b.loki_rope_table(None, 8, 64)
-    with pytest.raises(TypeError):
-        b.loki_rope_table("x", 8, 64, 10000.0, 1.0, None)
-    with pytest.raises(TypeError):
-        b.loki_rope_table(F, 8.5, 64, 10000.0, 1.0, None)
-    with pytest.raises(OverflowError):
-        b.loki_rope_table(F, 8, 1 << 40, 10000.0, 1.0, None)
-    assert b.loki_rope_table(None, 8, 64, 10000.0, 1.0, None) == 1  # the C entry's own refusals
-    with pytest.raises(TypeError):
-        b.empty_like(3)
+        b.dense(t)
+    with pytest.raises(TypeError, match="q must be a tensor"):
+        loki.dense_decode_attention_paged_q8(3, p8, p8, sc, sc, bt, bt[0])
+    with pytest.raises(TypeError, match="float8"):
+        loki.loki_append_keys_paged_q8(t, t, None, t, t, sc, sc, bt, bt[0])
+    with pytest.raises(TypeError, match="v_scales must be a tensor"):
+        loki.loki_append_keys_paged_q8(t, t, None, p8, p8, sc, None, bt, bt[0])
+    with pytest.raises(ValueError, match="v_scales must be torch.float32 \\[1, 1, 1\\]"):
+        loki.loki_append_keys_paged_q8(t, t, None, p8, p8, sc, sc.double(), bt, bt[0])
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        loki.loki_append_keys_paged_rope(t, t, None, t, t, bt, bt[0])
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        b.rope_table(torch.zeros(4, 16), 10000.0, 1.0)
 
 
 # --- the restatement's own pins -------------------------------------------------
