@@ -111,8 +111,6 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
     uint8_t* Bm = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     uint8_t* A = Bm + 4 * kAbAtom;
     float* angles = reinterpret_cast<float*>(A + 4 * kAbAtom);  // [128][rot_dim]
-    griddep_launch_dependents();
-
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tmem_slot))
                      : "memory");
@@ -124,6 +122,9 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
         mbar_init(&basis_bar, 1);
         fence_mbar_init();
     }
+    griddep_wait();  // launched early: inputs and pages may still be in use
+    fence_proxy_async_global();   // P and the angles come by bulk copies
+    griddep_launch_dependents();  // the stream of values and queries
     // this CTA's tiles: heads slowest, then sequences, then their runs
     auto runs_of = [&](int b) -> int64_t {
         const ApSeq s = append_seq(a, b, false);
@@ -427,7 +428,7 @@ static cudaError_t basis_impl(const AppendArgs& a, cudaStream_t s) {
     e = allow_dynamic_smem((const void*)kern, kAbSmem + kRunRows * 128 * 4);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (((int64_t)a.T + kRunRows - 2) / kRunRows + 1) * a.B * a.H_kv;
-    return launch_kernel(kern, dim3((unsigned)min64(tiles, di.sm_count)), dim3(kAbThreads), smem, s, false, a);
+    return launch_kernel(kern, dim3((unsigned)min64(tiles, di.sm_count)), dim3(kAbThreads), smem, s, true, a);
 }
 
 cudaError_t launch_append_basis(Dt dt, const AppendArgs& a, cudaStream_t s) {

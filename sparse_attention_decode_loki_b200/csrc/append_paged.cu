@@ -231,11 +231,13 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
     __shared__ __align__(8) uint64_t bar;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
     const bool lane_on = u < a.D >> 4;
-    griddep_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         fence_mbar_init();
     }
+    griddep_wait();  // launched early: inputs and pages may still be in use
+    fence_proxy_async_global();  // the angles come by bulk copies
+    griddep_launch_dependents();
     const int rot = a.rope != nullptr ? a.rot_dim : 0;
     const bool turn = u < rot >> 4;
     int ca, cb;
@@ -341,6 +343,7 @@ __global__ void __launch_bounds__(kRwThreads) k_append_rows(const AppendArgs a) 
     __shared__ float top[2][kRwRows];
     __shared__ int blk[kRwRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_wait();  // launched early: inputs and pages may still be in use
     if (blockIdx.x >= a.kv_ctas) {  // queries: one unit a thread
         const int64_t i = (int64_t)(blockIdx.x - a.kv_ctas) * kRwThreads + threadIdx.x;
         const int64_t r = i >> 3;
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(256) k_rope_table(float* __restrict__ table, i
 template <class E, bool kQ8, int D>
 static cudaError_t rows_impl(const AppendArgs& a, int64_t ctas, cudaStream_t s) {
     return launch_kernel(a.P != nullptr ? k_append_rows<E, kQ8, D, true> : k_append_rows<E, kQ8, D, false>,
-                         dim3((unsigned)ctas), dim3(kRwThreads), 0, s, false, a);
+                         dim3((unsigned)ctas), dim3(kRwThreads), 0, s, true, a);
 }
 
 template <class E, bool kQ8>
@@ -617,7 +620,7 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
         e = allow_dynamic_smem((const void*)kern, kRunRows * 128 * 4);
         if (e != cudaSuccess) return e;
         const size_t smem = a.rope != nullptr ? (size_t)kRunRows * a.rot_dim * sizeof(float) : 0;
-        e = launch_kernel(kern, dim3((unsigned)min64(runs * a.H_kv, di.sm_count)), dim3(kStThreads), smem, s, false, a);
+        e = launch_kernel(kern, dim3((unsigned)min64(runs * a.H_kv, di.sm_count)), dim3(kStThreads), smem, s, true, a);
     }
     if (e != cudaSuccess) return e;
     const int per_sm = E::kBytes == 2 ? 4 : 2;

@@ -311,3 +311,84 @@ def test_long_append_then_attention_without_a_pause(loki, cuda):
         torch.cuda.synchronize()
         assert torch.equal(o, alone[2])
     assert loki.loki_device_error(reset=True) == 0
+
+
+def test_calls_behind_copies_other_streams_and_joins(loki, cuda):
+    """The kernels are launched before their predecessors end and wait for them: inputs made just before
+    the call by a kernel, a copy, a fill or another stream, eager and captured with two streams joined."""
+    import torch
+    B, H, page, n = 3, 4, 32, 500
+    K8, V8, ks, vs, bt, sl = pool(torch, cuda, H, 128, page, 16, [n, 40, 0], 16, 58)
+    src = torch.randn(6, B, 2 * H, 128, generator=torch.Generator().manual_seed(59)).to(cuda)
+    host = src.cpu().pin_memory()
+    want = [loki.dense_decode_attention_paged_q8(x.contiguous(), K8, V8, ks, vs, bt, sl).clone() for x in src]
+    zero = loki.dense_decode_attention_paged_q8(torch.zeros_like(src[0]), K8, V8, ks, vs, bt, sl).clone()
+    torch.cuda.synchronize()
+    q, out = torch.empty_like(src[0]), torch.empty_like(src[0])
+    big = torch.zeros(64 << 20, device=cuda)
+    side = torch.cuda.Stream()
+
+    def call():
+        return loki.dense_decode_attention_paged_q8(q, K8, V8, ks, vs, bt, sl, out=out)
+
+    got = []
+    for i in range(6):
+        big.add_(1.0)  # keeps the device busy, so that what follows is queued
+        q.copy_(src[i])
+        got.append(call().clone())
+        big.add_(1.0)
+        q.copy_(host[i], non_blocking=True)
+        got.append(call().clone())
+        big.add_(1.0)
+        q.zero_()
+        got.append(call().clone())
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big.add_(1.0)
+            q.copy_(src[(i + 1) % 6])
+        torch.cuda.current_stream().wait_stream(side)
+        got.append(call().clone())
+    torch.cuda.synchronize()
+    for i in range(6):
+        for g, w in zip(got[4 * i:4 * i + 4], (want[i], want[i], zero, want[(i + 1) % 6])):
+            assert torch.equal(g, w), i
+
+    T = 40
+    s = make(torch, cuda, 1, 2, 2, T, 128, 16, [0], [T], torch.bfloat16, True, 128, 32, 16, 60)
+    one = make(torch, cuda, 1, 2, 2, 1, 128, 16, [T], [1], torch.bfloat16, True, 128, 32, 0, 61)
+    bt2 = torch.arange(3, dtype=torch.int32, device=cuda)[None].contiguous()
+    tab = table_for(loki, cuda, T + 1, 128)
+    pages = [torch.zeros(3, 2, 16, 128, dtype=torch.uint8, device=cuda).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones(3, 2, 1, device=cuda) for _ in range(2)]
+    length = torch.zeros(1, dtype=torch.int32, device=cuda)
+    qo, ao = torch.empty_like(one["q"]), torch.empty(1, 4, 128, device=cuda, dtype=torch.bfloat16)
+
+    def steps():
+        length.zero_()
+        loki.loki_append_keys_paged_q8(s["K"], s["V"], s["P"], *pages, *scales, bt2, length, rope_table=tab)
+        length.add_(T)
+        loki.loki_append_keys_paged_q8(one["K"], one["V"], s["P"], *pages, *scales, bt2, length, rope_table=tab, q=one["q"], q_out=qo)
+        length.add_(1)
+        loki.dense_decode_attention_paged_q8(qo.view(1, 4, 128), *pages, *scales, bt2, length, out=ao)
+
+    def result():
+        torch.cuda.synchronize()
+        return [t.view(torch.uint8).clone() if t.dtype == torch.float8_e4m3fn else t.clone() for t in (*pages, *scales, qo, ao)]
+
+    steps()
+    eager = result()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big[:1024].add_(1.0)
+        big[2048:4096].add_(1.0)
+        torch.cuda.current_stream().wait_stream(side)  # two nodes before the first call
+        steps()
+        steps()
+    for _ in range(3):
+        for t in (*pages, *scales, qo, ao):
+            (t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t).zero_()
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(result(), eager))
+    assert loki.loki_device_error(reset=True) == 0
