@@ -119,17 +119,26 @@ loki_dtype dtype_of(at::ScalarType t) {
     refuse(PyExc_TypeError, "unsupported dtype %s: use torch.float32 or torch.bfloat16", type_name(t).c_str());
 }
 
-// `call` (which must not throw: the interpreter lock is released) on the
-// device's current stream, the device being the current one
+// the interpreter lock, released for a scope (reading a tensor's address may throw)
+struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// `call` on the device's current stream, the device being the current one
 template <class F>
 loki_status launch(int device, F call) {
     const c10::cuda::CUDAGuard guard(device);
     void* stream = c10::cuda::getCurrentCUDAStream(device).stream();
-    loki_status st;
-    Py_BEGIN_ALLOW_THREADS;
-    st = call(stream);
-    Py_END_ALLOW_THREADS;
-    return st;
+    const Unlocked unlocked;
+    return call(stream);
+}
+
+// a new reference to the tensor argument that was given, or to the fresh tensor in its place
+PyObject* object(PyObject* o, Ten given, const at::Tensor& fresh) {
+    if (given == nullptr) return THPVariable_Wrap(fresh);
+    Py_INCREF(o);
+    return o;
 }
 
 // 8-bit pages and their scales: the tokens of a scale block
@@ -158,6 +167,8 @@ PyObject* append(Args o, PyObject** out_obj) {
     Ten q = tensor(o[13], "q", true), q_out = tensor(o[14], "q_out", true);
     const int block = q8 ? check_q8(Kp, Vp, ks, vs) : 0;
     const int device = place({K, V, P, Kp, Vp, ks, vs, bt, pos, rope, lo, new_lens, q, q_out});
+    for (Ten t : {P, rope, lo, new_lens, q, q_out})  // (a null address would mean: not given)
+        if (t != nullptr && ptr(t) == nullptr) refuse(PyExc_ValueError, "an optional tensor is given, but has no elements (or no memory)");
     if (K->dim() != 4 || Kp->dim() != 4 || bt->dim() != 2)
         refuse(PyExc_ValueError,
                "K_new [B, H_kv, T, D], pages [n_pages, H_kv, page_size, D] and block_table [B, max_pages] expected");
@@ -209,15 +220,7 @@ PyObject* append(Args o, PyObject** out_obj) {
                                                 iq, ptr(Kp), ptr(Vp), ptr(lo), il, i32(bt), i32(pos), i32(new_lens), iB,
                                                 iH, iT, ip, im, n_pages, iD, dt, stream);
     });
-    if (q == nullptr) {
-        Py_INCREF(Py_None);
-        *out_obj = Py_None;
-    } else if (fresh.defined()) {
-        *out_obj = THPVariable_Wrap(fresh);
-    } else {
-        Py_INCREF(o[14]);
-        *out_obj = o[14];
-    }
+    *out_obj = object(o[14], fresh.defined() ? nullptr : K, fresh);  // (o[14] is None without q)
     return PyLong_FromLong(st);
 }
 
@@ -262,18 +265,6 @@ at::Tensor workspace(Ten given, size_t need, const at::Tensor& like) {
     return t;
 }
 
-// the output given, or a fresh one; its Python object in *obj
-at::Tensor output(PyObject* o, Ten given, at::IntArrayRef shape, const at::TensorOptions& options, PyObject** obj) {
-    if (given != nullptr) {
-        Py_INCREF(o);
-        *obj = o;
-        return *given;
-    }
-    at::Tensor t = at::empty(shape, options);
-    *obj = THPVariable_Wrap(t);
-    return t;
-}
-
 // dense(q, K8, V8, k_scales, v_scales, block_table, seq_lens, scale, out, workspace): (status, out)
 PyObject* dense(Args o, PyObject** out_obj) {
     Ten out = tensor(o[8], "out", true), ws = tensor(o[9], "workspace", true);
@@ -283,13 +274,15 @@ PyObject* dense(Args o, PyObject** out_obj) {
     expect(out, "out", a.q->scalar_type(), a.q->sizes());
     const at::Tensor w = workspace(
         ws, dense_decode_paged_q8_workspace_size(a.B, a.H_q, a.H_kv, a.page_size, a.max_pages, a.D), *a.q);
-    const at::Tensor r = output(o[8], out, a.q->sizes(), a.q->options(), out_obj);
-    return PyLong_FromLong(launch(a.device, [&](void* stream) {
+    const at::Tensor r = out != nullptr ? *out : at::empty(a.q->sizes(), a.q->options());
+    const loki_status st = launch(a.device, [&](void* stream) {
         return dense_decode_attention_paged_q8(a.q->data_ptr(), a.K8->data_ptr(), a.V8->data_ptr(), a.scales(a.ks),
                                                a.scales(a.vs), a.block, a.ints(a.bt), a.ints(a.sl), a.B, a.H_q, a.H_kv,
                                                a.page_size, a.max_pages, a.n_pages, a.D, scale, dt, r.data_ptr(),
                                                w.data_ptr(), w.nbytes(), stream);
-    }));
+    });
+    *out_obj = object(o[8], out, r);
+    return PyLong_FromLong(st);
 }
 
 // sparse(q_rot, K8, V8, k_scales, v_scales, block_table, seq_lens, selected_idx, scale, dtype, out, workspace)
@@ -306,13 +299,15 @@ PyObject* sparse(Args o, PyObject** out_obj) {
     expect(out, "out", type, a.q->sizes());
     const float scale = (float)real(o[8]);
     const at::Tensor w = workspace(ws, loki_sparse_attention_paged_q8_workspace_size(a.B, a.H_q, a.H_kv, k, a.D), *a.q);
-    const at::Tensor r = output(o[10], out, a.q->sizes(), a.q->options().dtype(type), out_obj);
-    return PyLong_FromLong(launch(a.device, [&](void* stream) {
+    const at::Tensor r = out != nullptr ? *out : at::empty(a.q->sizes(), a.q->options().dtype(type));
+    const loki_status st = launch(a.device, [&](void* stream) {
         return loki_sparse_attention_paged_q8(static_cast<const float*>(a.q->data_ptr()), a.K8->data_ptr(), a.V8->data_ptr(),
                                               a.scales(a.ks), a.scales(a.vs), a.block, a.ints(a.bt), a.ints(a.sl),
                                               a.ints(idx), a.B, a.H_q, a.H_kv, a.page_size, a.max_pages, a.n_pages, a.D, k,
                                               scale, dt, r.data_ptr(), w.data_ptr(), w.nbytes(), stream);
-    }));
+    });
+    *out_obj = object(o[10], out, r);
+    return PyLong_FromLong(st);
 }
 
 // decode(q, K8, V8, k_scales, v_scales, block_table, seq_lens, plane, P, d, k, scale, out, selected_idx, workspace):
@@ -334,18 +329,18 @@ PyObject* decode(Args o, PyObject** out_obj) {
     const float scale = (float)real(o[11]);
     const at::Tensor w = workspace(
         ws, loki_paged_q8_decode_workspace_size(a.B, a.H_q, a.H_kv, a.page_size, a.max_pages, a.D, d, k), *a.q);
-    PyObject *po = nullptr, *pi = nullptr;
-    const at::Tensor r = output(o[12], out, a.q->sizes(), a.q->options(), &po);
-    const at::Tensor si = output(o[13], idx, {a.B, a.H_q, k}, a.q->options().dtype(at::kInt), &pi);
-    *out_obj = PyTuple_Pack(2, po, pi);
-    Py_DECREF(po);
-    Py_DECREF(pi);
-    return PyLong_FromLong(launch(a.device, [&](void* stream) {
+    const at::Tensor r = out != nullptr ? *out : at::empty(a.q->sizes(), a.q->options());
+    const at::Tensor si = idx != nullptr ? *idx : at::empty({a.B, a.H_q, k}, a.q->options().dtype(at::kInt));
+    const loki_status st = launch(a.device, [&](void* stream) {
         return loki_decode_attention_paged_q8(a.q->data_ptr(), a.K8->data_ptr(), a.V8->data_ptr(), a.scales(a.ks),
-                                              a.scales(a.vs), a.block, lo->data_ptr(), il, a.scales(P), a.ints(a.bt), a.ints(a.sl), a.B, a.H_q, a.H_kv, a.page_size,
-                                              a.max_pages, a.n_pages, a.D, d, k, scale, dt, r.data_ptr(),
-                                              static_cast<int32_t*>(si.data_ptr()), w.data_ptr(), w.nbytes(), stream);
-    }));
+                                              a.scales(a.vs), a.block, lo->data_ptr(), il, a.scales(P), a.ints(a.bt),
+                                              a.ints(a.sl), a.B, a.H_q, a.H_kv, a.page_size, a.max_pages, a.n_pages,
+                                              a.D, d, k, scale, dt, r.data_ptr(), static_cast<int32_t*>(si.data_ptr()),
+                                              w.data_ptr(), w.nbytes(), stream);
+    });
+    // ("N" takes the new references)
+    *out_obj = Py_BuildValue("(NN)", object(o[12], out, r), object(o[13], idx, si));
+    return PyLong_FromLong(st);
 }
 
 // rope_table(table, base, pos_scale): (status, None)

@@ -392,3 +392,61 @@ def test_calls_behind_copies_other_streams_and_joins(loki, cuda):
         g.replay()
         assert all(torch.equal(a, b) for a, b in zip(result(), eager))
     assert loki.loki_device_error(reset=True) == 0
+
+
+def test_tensors_without_memory_are_an_error(loki, cuda):
+    """Tensors that stand for shapes only (their addresses cannot be read): an exception, no launch."""
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        q = torch.empty(1, 2, 128, device=cuda)
+        p8 = torch.empty(2, 2, 16, 128, device=cuda, dtype=torch.float8_e4m3fn)
+        sc = torch.empty(2, 2, 1, device=cuda)
+        bt, n = (torch.empty(*s, device=cuda, dtype=torch.int32) for s in ((1, 2), (1,)))
+        idx = torch.empty(1, 2, 4, device=cuda, dtype=torch.int32)
+        plane, P = torch.empty(2, 2, 16, 16, device=cuda), torch.empty(2, 128, 128, device=cuda)
+        new, tab = torch.empty(1, 2, 1, 128, device=cuda), torch.empty(8, 128, device=cuda)
+    pages = (p8, p8, sc, sc, bt, n)
+    for call in (lambda: loki.dense_decode_attention_paged_q8(q, *pages),
+                 lambda: loki.loki_sparse_attention_paged_q8(q, *pages, idx),
+                 lambda: loki.loki_decode_attention_paged_q8(q, *pages[:4], plane, P, bt, n, 16, 4),
+                 lambda: loki.loki_append_keys_paged_q8(new, new, P, *pages, rope_table=tab),
+                 lambda: loki.loki_append_keys_paged_rope(new, new, P, plane.new_empty(2, 2, 16, 128),
+                                                          plane.new_empty(2, 2, 16, 128), bt, n)):
+        with pytest.raises((RuntimeError, ValueError)):  # (a null address, or one that the type refuses to give)
+            call()
+    torch.cuda.synchronize()
+    assert loki.loki_device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("T", [16, 17, 300])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("q8", [False, True], ids=["dt", "q8"])
+def test_queries_in_place_in_all_forms(loki, cuda, T, inter, q8):
+    """q_out may be q: the same bits, in single rows, tiles and streams, tokens left out included."""
+    import torch
+    lens = [T, 0, T // 2]
+    s = make(torch, cuda, 3, 2, 4, T, 128, 64, [0, 5, 40], lens, torch.bfloat16, q8, 96, 0, 16 if q8 else 0, 51)
+    tab = table_for(loki, cuda, 512, 96)
+    for P in (None, s["P"]):
+        pages = (s["Kp"], s["Vp"]) + ((s["ks"], s["vs"]) if q8 else ())
+        f = loki.loki_append_keys_paged_q8 if q8 else loki.loki_append_keys_paged_rope
+        q = s["q"].clone()
+        apart = q.clone()
+        kw = dict(rope_table=tab, interleaved=inter, new_lens=s["new"])
+        f(s["K"], s["V"], P, *pages, s["bt"], s["pos"], q=s["q"], q_out=apart, **kw)
+        got = f(s["K"], s["V"], P, *pages, s["bt"], s["pos"], q=q, q_out=q, **kw)
+        assert got is q and torch.equal(q, apart) and torch.equal(q[1], s["q"][1])
+
+
+@pytest.mark.parametrize("what", ["rope_table", "Kt_lo_pages", "new_lens", "q"])
+def test_empty_optional_tensors_are_refused(loki, cuda, what):
+    """An empty table is no missing table: nothing is appended unrotated."""
+    import torch
+    s = make(torch, cuda, 1, 2, 1, 3, 128, 16, [0], [3], torch.bfloat16, False, 128, 0, 0, 61)
+    was = s["Kp"].clone()
+    empty = {"rope_table": torch.empty(0, 128, device=cuda), "Kt_lo_pages": s["Kp"][..., :0].contiguous(),
+             "new_lens": s["new"][:0], "q": s["q"][:, :0]}[what]
+    with pytest.raises(ValueError):
+        loki.loki_append_keys_paged_rope(s["K"], s["V"], None, s["Kp"], s["Vp"], s["bt"], s["pos"], **{what: empty})
+    assert torch.equal(s["Kp"], was)
