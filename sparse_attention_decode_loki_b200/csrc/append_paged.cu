@@ -329,8 +329,9 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
 // CTA per KV head and group of sequences, at most 16 rows. A quarter of a
 // basis column sits in each thread's registers, loaded before anything else;
 // a warp per row turns it, quantises it and stores it. 16 sequences of 40 heads:
-// 4.4 us (8 bits 5.2); in two waves of CTAs it took 8.0 (9.3), in two CTAs an SM
-// of 64 registers 6.2 (7.1).
+// 4.2 us (8 bits 4.9), call after call. Before the launch was hidden behind the
+// preceding call: 4.4 (5.2), in two waves of CTAs 8.0 (9.3), in two CTAs an SM of
+// 64 registers 6.2 (7.1).
 
 constexpr int kRwThreads = 512, kRwRows = kRwThreads / 32;  // a row to a warp
 
