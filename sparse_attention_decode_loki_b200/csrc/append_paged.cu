@@ -19,14 +19,16 @@ namespace loki {
 // scale blocks of more than 16 tokens belong to neighbouring warps, which share
 // their largest magnitude through shared memory, so every scale has one owner.
 // Queries: a warp has four positions, whose angles stay in its registers while
-// it goes through the heads.
+// it goes through the heads; their rows lie together, 1 KB of bf16 a head, which
+// a ring of bulk copies per warp brings.
 //
 // Measured on two prompts of 8192 and 6144 tokens, 32 query and 8 KV heads, into
-// 8 bits: 55 us for values and queries (279 MB, 5.1 TB/s), 35 us for keys, 77 us
-// side by side. Rows of all heads in one 16-row warp item with the angles in
-// shared memory took 103 us, U = 3 or 4 heads in flight 84 to 86.
+// 8 bits, values, queries (279 MB) and keys side by side: 62 us (5.3 TB/s). A
+// ring of 3 heads 65, of 4 66; bulk stores as well 64; query loads into
+// registers (2 heads ahead) 76, 3 or 4 ahead 84 to 86; rows of all heads in one
+// 16-row warp item with the angles in shared memory 103.
 
-constexpr int kStThreads = 256, kStQueryRows = 32;
+constexpr int kStThreads = 256, kStQueryRows = 32, kStQueryStages = 2;
 
 // a warp's 16 positions of a run and their place in the pool but for the head's
 // offset (the page is the same for all heads)
@@ -102,6 +104,8 @@ template <class E, bool kQ8>
 __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_stream(const AppendArgs a) {
     using Tp = typename E::T;
     __shared__ float red[2][kStThreads / 32];
+    extern __shared__ __align__(16) uint8_t ring[];  // the queries', per warp
+    __shared__ __align__(8) uint64_t full[kStThreads / 32][kStQueryStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
     const bool lane_on = u < a.D >> 4;
     if ((int)blockIdx.x >= a.kv_ctas) {
@@ -109,44 +113,67 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_s
         const int q = blockIdx.x - a.kv_ctas, blocks = (a.T + kStQueryRows - 1) / kStQueryRows, b = q / blocks % a.B;
         const int t = q % blocks * kStQueryRows + 4 * warp + sub, chunk = q / blocks / a.B;
         const int h0 = chunk * a.q_group, h1 = min(h0 + a.q_group, a.H_q);
-        const bool here = lane_on && t < a.T;
         int ca, cb;
         const bool turn = a.rope != nullptr && u < a.rot_dim >> 4;
         unit_cols(turn ? a.rot_dim : 0, a.interleaved, u, &ca, &cb);
         const int64_t step = (int64_t)a.T * a.D, at = (((int64_t)b * a.H_q + h0) * a.T + t) * a.D;
         const Tp* p = static_cast<const Tp*>(a.q) + at;
         Tp* o = static_cast<Tp*>(a.q_out) + at;
-        // U heads are on their way; a head's registers take the one U behind it as soon as it is unpacked
-        constexpr int U = 2;
-        Chunk<E> wa[U], wb[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (here && h0 + i < h1) {
-                wa[i].load(p + i * step + ca);
-                wb[i].load(p + i * step + cb);
-            }
-        const int64_t j = (int64_t)__ldg(a.positions + b) + t;
+        // The warp's rows r0 .. r1 - 1 of its four are appended. They lie together: a bulk copy a head, S
+        // heads on their way.
+        constexpr int S = kStQueryStages, kSlot = 4 * 128 * E::kBytes;
+        uint8_t* const slots = ring + warp * S * kSlot;
+        const int t0 = t - sub;
+        const int64_t j0 = (int64_t)__ldg(a.positions + b) + t0;
         const int n = a.new_lens != nullptr ? min(__ldg(a.new_lens + b), a.T) : a.T;
-        if (here && t < n && j >= 0 && (a.rope == nullptr || j < a.n_pos)) {
+        const int r0 = (int)min64(j0 < 0 ? -j0 : 0, 4);
+        const int64_t end = min64(min64(4, (int64_t)n - t0), a.rope != nullptr ? a.n_pos - j0 : 4);
+        const int r1 = end > r0 ? (int)end : r0, row = a.D * E::kBytes;
+        const uint32_t bytes = (r1 - r0) * row;
+        if (bytes > 0) {
+            if (lane == 0) {
+                for (int i = 0; i < S; ++i) mbar_init(&full[warp][i], 1);
+                fence_mbar_init();
+                fence_proxy_async_global();
+            }
+            __syncwarp();
+            const Tp* src = p + (r0 - sub) * (int64_t)a.D;
+            auto issue = [&](int h, int i) {
+                mbar_arrive_expect_tx(&full[warp][i], bytes);
+                bulk_load(slots + i * kSlot + r0 * row, src + (h - h0) * step, bytes, &full[warp][i]);
+            };
+            if (lane == 0)
+                for (int i = 0; i < S && h0 + i < h1; ++i) issue(h0 + i, i);
+            const bool mine = lane_on && sub >= r0 && sub < r1;
             Angles g;
-            if (turn) g.load(a.rope + j * a.rot_dim, a.rot_dim, u);
-            for (int h = h0; h < h1; h += U) {
+            if (turn && mine) g.load(a.rope + (j0 + sub) * a.rot_dim, a.rot_dim, u);
+            int i = 0, h = h0;
+            uint32_t phase = 0;
+            for (; h < h1; ++h) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][i], phase, a.err))) break;
+                float x[16];
+                if (mine) {
+                    const uint8_t* in = slots + i * kSlot + sub * row;
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (h + i < h1) {
-                        float x[16];
-                        wa[i].get(x);
-                        wb[i].get(x + 8);
-                        if (h + i + U < h1) {
-                            wa[i].load(p + (i + U) * step + ca);
-                            wb[i].load(p + (i + U) * step + cb);
-                        }
-                        if (turn) g.turn(x, a.interleaved);
-                        store_chunk<E>(o + i * step + ca, x, ca, a.D);
-                        store_chunk<E>(o + i * step + cb, x + 8, cb, a.D);
+                    for (int e = 0; e < Chunk<E>::kN; ++e) {
+                        E::unpack(reinterpret_cast<const uint4*>(in + ca * E::kBytes)[e], x + e * E::kVec);
+                        E::unpack(reinterpret_cast<const uint4*>(in + cb * E::kBytes)[e], x + 8 + e * E::kVec);
                     }
-                p += U * step;
-                o += U * step;
+                }
+                __syncwarp();
+                if (lane == 0 && h + S < h1) issue(h + S, i);
+                if (mine) {
+                    if (turn) g.turn(x, a.interleaved);
+                    store_chunk<E>(o + ca, x, ca, a.D);
+                    store_chunk<E>(o + cb, x + 8, cb, a.D);
+                }
+                o += step;
+                if (++i == S) i = 0, phase ^= 1;
+            }
+            // every copy has landed before the CTA may end
+            for (int l = h + 1; l < min(h + S, h1); ++l) {
+                if (++i == S) i = 0, phase ^= 1;
+                mbar_wait(&full[warp][i], phase, a.err);
             }
         }
     } else {
@@ -637,7 +664,11 @@ static cudaError_t append_impl(AppendArgs a, cudaStream_t s) {
     }
     if (runs * a.chunks + q_ctas > 0x7fffffff) return cudaErrorInvalidValue;
     a.kv_ctas = (int)(runs * a.chunks);
-    return launch_kernel(k_append_stream<E, kQ8>, dim3((unsigned)(a.kv_ctas + q_ctas)), dim3(kStThreads), 0, s, true, a);
+    auto kern = k_append_stream<E, kQ8>;
+    const size_t ring = a.q != nullptr ? (size_t)kStQueryRows * kStQueryStages * 128 * E::kBytes : 0;
+    e = allow_dynamic_smem((const void*)kern, ring);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3((unsigned)(a.kv_ctas + q_ctas)), dim3(kStThreads), ring, s, true, a);
 }
 
 cudaError_t launch_append_paged(Dt dt, AppendArgs a, cudaStream_t s) {

@@ -450,3 +450,35 @@ def test_empty_optional_tensors_are_refused(loki, cuda, what):
     with pytest.raises(ValueError):
         loki.loki_append_keys_paged_rope(s["K"], s["V"], None, s["Kp"], s["Vp"], s["bt"], s["pos"], **{what: empty})
     assert torch.equal(s["Kp"], was)
+
+
+@pytest.mark.parametrize("T", [12, 40])
+@pytest.mark.parametrize("D,dtn", [(128, "bf16"), (96, "bf16"), (128, "f32")])
+def test_queries_at_the_ends_of_the_positions(loki, cuda, T, D, dtn):
+    """Positions below zero or behind the angle table, and new_lens, cut a sequence's rows anywhere: the
+    others' queries are turned, theirs are left."""
+    import torch
+    dt = torch.bfloat16 if dtn == "bf16" else torch.float32
+    pos, new, n_pos = [-3, 7, -50, 0, -6], [T, T - 5, T, 3, T], 7 + T - 9
+    s = make(torch, cuda, 5, 2, 3, T, D, 16, [0] * 5, [0] * 5, dt, False, 96, 0, 0, 71)
+    s["bt"].fill_(-1)  # no pages: only the queries have a place to go
+    tab = table_for(loki, cuda, n_pos, 96)
+    q_out = torch.full_like(s["q"], 7.0)
+    i32 = lambda x: torch.tensor(x, device=cuda, dtype=torch.int32)  # noqa: E731
+    loki.loki_append_keys_paged_rope(s["K"], s["V"], None, s["Kp"], s["Vp"], s["bt"], i32(pos), rope_table=tab,
+                                     new_lens=i32(new), q=s["q"], q_out=q_out)
+    torch.cuda.synchronize()
+    loki.loki_device_error(reset=True)  # (tokens without a place are flagged)
+    q, got, t64 = f64(s["q"]), f64(q_out), f64(tab)
+    for b in range(5):
+        for t in range(T):
+            j = pos[b] + t
+            if j < 0 or j >= n_pos or t >= new[b]:
+                assert np.all(got[b, :, t] == 7.0), (b, t)
+                continue
+            x, c, sn = q[b, :, t], t64[j, :48], t64[j, 48:]
+            want = x.copy()
+            want[:, :48] = x[:, :48] * c - x[:, 48:96] * sn
+            want[:, 48:96] = x[:, :48] * sn + x[:, 48:96] * c
+            # two fp32 roundings of products of two, then one to dt
+            check_rows(torch, got[b, :, t], want, dt, 2.0 ** -23 * 2 * np.abs(x).max())
