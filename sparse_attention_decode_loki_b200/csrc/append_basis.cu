@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
         w += left;
         // P, as it is, to where A will be; two threads to a column, half of its rows each: the largest
         // magnitude, then the parts
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_proxy_async_shared();
         __syncthreads();  // the last head's product and staged rows are done with
         if (tid == 0) {
             mbar_arrive_expect_tx(&basis_bar, D * D * 4);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
                     put_parts(Bm, c, i0 + i, x, pow2(e));
                 }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fence_proxy_async_shared();
             alive = !__syncthreads_or(!alive);
         }
         for (; alive && left > 0; --left) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
                     put_parts(A, r, cb, x + 8, pow2(e));
                 }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fence_proxy_async_shared();
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncthreads();
             if (tid == 0) {

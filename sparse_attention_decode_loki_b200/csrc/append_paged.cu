@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_s
                         E::unpack(reinterpret_cast<const uint4*>(in + cb * E::kBytes)[e], x + 8 + e * E::kVec);
                     }
                 }
+                fence_proxy_async_shared();  // the rows are read before the next head's arrive
                 __syncwarp();
                 if (lane == 0 && h + S < h1) issue(h + S, i);
                 if (mine) {
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
         w += h1 - h0;
         const ApSeq sq = append_seq(a, b, false);
         const int64_t start = (sq.lo / kRunRows + (ri - before)) * kRunRows;
+        fence_proxy_async_shared();
         __syncthreads();  // the run before is done with its angles (and the barrier is set up)
         if (rot > 0 && threadIdx.x == 0) {
             const uint32_t bytes = (uint32_t)min64(sq.hi - start, kRunRows) * rot * 4;

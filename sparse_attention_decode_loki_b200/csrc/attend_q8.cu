@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
     uint32_t phase = 0;
     bool alive = true;
     for (int at = 0; w < w_end; phase ^= at + 1 == kStages, at = at + 1 == kStages ? 0 : at + 1) {
+        fence_proxy_async_shared();
         __syncwarp();  // every lane is done with the stage before this one
         if (w + kStages - 1 < w_end) tile[kStages - 1] = load(at == 0 ? kStages - 1 : at - 1);
         const float ks1 = __ldg(a.k_scales + tile[1].blk), vs1 = __ldg(a.v_scales + tile[1].blk);

@@ -115,6 +115,13 @@ __device__ __forceinline__ void fence_proxy_async_global() {
     asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
+// order this thread's earlier reads and writes of shared memory before bulk
+// copies into or out of it that are issued behind the next barrier: a barrier
+// among threads alone lets a copy overtake a read that is still queued
+__device__ __forceinline__ void fence_proxy_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // named barrier over `count` threads (a multiple of 32), id 1..15
 __device__ __forceinline__ void named_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");

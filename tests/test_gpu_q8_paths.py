@@ -482,3 +482,24 @@ def test_queries_at_the_ends_of_the_positions(loki, cuda, T, D, dtn):
             want[:, 48:96] = x[:, :48] * sn + x[:, 48:96] * c
             # two fp32 roundings of products of two, then one to dt
             check_rows(torch, got[b, :, t], want, dt, 2.0 ** -23 * 2 * np.abs(x).max())
+
+
+@pytest.mark.parametrize("dtn,H,T", [("f32", 40, 2312), ("bf16", 32, 4096)])
+def test_queries_of_long_prompts_call_after_call(loki, cuda, dtn, H, T):
+    """Many heads of rows that stay in the cache, again and again: the rings' slots are read before they
+    are filled anew."""
+    import torch
+    dt = torch.bfloat16 if dtn == "bf16" else torch.float32
+    s = make(torch, cuda, 1, 8, H // 8, T, 128, 48, [20], [T], dt, False, 128, 32, 0, 81)
+    tab = table_for(loki, cuda, 20 + T, 128)
+    outs = torch.zeros(60, *s["q"].shape, device=cuda, dtype=dt) if dtn == "bf16" else torch.zeros(40, *s["q"].shape, device=cuda)
+    for o in outs:
+        loki.loki_append_keys_paged_rope(s["K"], s["V"], None, s["Kp"], s["Vp"], s["bt"], s["pos"], rope_table=tab,
+                                         Kt_lo_pages=s["lo"], q=s["q"], q_out=o)
+    x, c, sn = s["q"].double(), tab[20:, :64].double(), tab[20:, 64:].double()
+    want = torch.cat([x[..., :64] * c - x[..., 64:] * sn, x[..., :64] * sn + x[..., 64:] * c], dim=-1)
+    # fp32: two roundings of at most |a c| + |b s| each; then one to dt
+    bound = 2.0 ** -23 * 2 * float(x.abs().max())
+    tol = torch.finfo(dt).eps / 2 * (want.abs() + bound) + bound
+    for i, o in enumerate(outs):
+        assert bool(((o.double() - want).abs() <= tol).all()), i
