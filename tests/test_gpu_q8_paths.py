@@ -503,3 +503,29 @@ def test_queries_of_long_prompts_call_after_call(loki, cuda, dtn, H, T):
     tol = torch.finfo(dt).eps / 2 * (want.abs() + bound) + bound
     for i, o in enumerate(outs):
         assert bool(((o.double() - want).abs() <= tol).all()), i
+
+
+def test_first_calls_of_new_processes(cuda):
+    """The first call of a process, its memory and code cold, is where a slot filled too early showed."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, sparse_attention_decode_loki_b200 as loki
+g = torch.Generator().manual_seed(91)
+T, H = 2312, 40
+q = torch.randn(1, H, T, 128, generator=g).cuda()
+new = torch.randn(1, 8, T, 128, generator=g).cuda()
+pages = torch.zeros(49, 8, 48, 128, device="cuda")
+tab = loki.loki_rope_table(T, 128, device="cuda")
+bt, pos = torch.arange(49, device="cuda", dtype=torch.int32)[None], torch.zeros(1, device="cuda", dtype=torch.int32)
+got = loki.loki_append_keys_paged_rope(new, new, None, pages, pages.clone(), bt, pos, rope_table=tab, q=q)
+x, c, s = q.double(), tab[:, :64].double(), tab[:, 64:].double()
+want = torch.cat([x[..., :64] * c - x[..., 64:] * s, x[..., :64] * s + x[..., 64:] * c], dim=-1)
+bound = 2.0 ** -22 * float(x.abs().max())  # three fp32 roundings of at most |a c| + |b s| each
+assert bool(((got.double() - want).abs() <= bound).all())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(2):
+        jobs = [subprocess.Popen([sys.executable, "-c", code], cwd=root) for _ in range(4)]
+        assert [j.wait(timeout=300) for j in jobs] == [0] * 4
