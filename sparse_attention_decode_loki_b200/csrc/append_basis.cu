@@ -23,7 +23,7 @@
 // took 1.5 us a tile). Rows that hold an infinity or a NaN take the plain fp32
 // sum instead (an infinity has no second part).
 //
-// Measured on a 4096-token prompt of 32 heads into 8 bits: 53 us alone, 64 us
+// Measured on a 4096-token prompt of 32 heads into 8 bits: 53 us alone, 63 us
 // with the stream (27 alone) beside it; 7 us a tile, of which 1.7 us turn and
 // split, 1.2 us products, 1.6 us the two passes over the product, 0.7 us copies.
 // Latencies of these phases bound it (36 % of issue slots, 13 % of the tensor
