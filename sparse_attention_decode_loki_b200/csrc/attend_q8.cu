@@ -24,13 +24,14 @@
 //
 // Softmax in base 2, in fp32, against references that move rarely: a head's
 // weights are u = 2^(x - m) for the sum and w = u s_V 2^-E for the product; m
-// and the whole number E are raised (and the sums scaled down) only when a
+// and the even number E are raised (and the sums scaled down) only when a
 // score lies 8 above m or a weight would pass 2^15, fp16's range. So a tile
 // costs one warp vote instead of a maximum over its lanes, and the product
 // stays in the tensor cores' accumulators from tile to tile. E is set so that
 // the largest weight so far is 1/2 or more: a weight's rounding, 2^-22 of
 // itself or 2^-25, is 2^-24 of the largest weighted value at most, whatever
-// the scales of the other blocks.
+// the scales of the other blocks. 2^-E is held as its root and multiplied in
+// twice: it and its inverse would leave fp32 for scales near fp32's ends.
 //
 // A warp keeps kStages tiles in a ring of its own in shared memory, two of
 // them on their way (128 KB in flight per SM): dense tiles, 16 rows of one
@@ -108,6 +109,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// 1 / x of a power of two
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // box {D, 16} of a [rows, D] byte matrix, from its row `row` on
 __device__ __forceinline__ void tile_load(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {
@@ -214,8 +218,8 @@ struct PickStage : Frag<D> {
 // NT groups of up to four query heads of one KV head: their query fragments,
 // softmax state and output accumulators. Lane (gid, tig) accumulates head
 // 4 t + tig, columns gid D / 8 .., hi and lo parts apart, in units of 2^(m + E);
-// m and lift = 2^-E are the same in the eight lanes of a head, l is the lane's
-// own tokens' share.
+// m and lift = 2^(-E / 2) are the same in the eight lanes of a head, l is the
+// lane's own tokens' share.
 template <int D, int NT>
 struct Heads {
     static constexpr int KW = Frag<D>::KW, VW = Frag<D>::VW;
@@ -320,7 +324,7 @@ struct Heads {
             const float x0 = ok0 ? ((c[t][0][0] + c[t][1][0]) + (c[t][0][1] + c[t][1][1])) * qs[t] * k0 : -INFINITY;
             const float x1 = ok1 ? ((c[t][0][2] + c[t][1][2]) + (c[t][0][3] + c[t][1][3])) * qs[t] * k1 : -INFINITY;
             float u0 = exp2_fast(x0 - m[t]), u1 = exp2_fast(x1 - m[t]);
-            float w0 = u0 * lift[t] * v0, w1 = u1 * lift[t] * v1;
+            float w0 = u0 * lift[t] * v0 * lift[t], w1 = u1 * lift[t] * v1 * lift[t];
             const float top = fmaxf(x0, x1);
             if (__any_sync(0xffffffffu, top > m[t] + 8.f || fmaxf(w0, w1) > 32768.f)) {
                 float M = fmaxf(m[t], top);
@@ -331,13 +335,15 @@ struct Heads {
                 float y = fmaxf(u0 * v0, u1 * v1);
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
-                // this tile's largest weighted value lies in 2^(M + E), 2^(M + E + 1), the others' in
-                // units of 2^(m + E before); 2^-E and its inverse stay far from fp32's ends
-                int E = max((int)(__float_as_uint(y) >> 23) - 127, -100);
+                // this tile's largest weighted value lies in 2^(M + E), 2^(M + E + 2), the others' in
+                // units of 2^(m + E before)
+                int H = max(((int)(__float_as_uint(y) >> 23) - 127) >> 1, -63);  // E / 2
+                const int was = 127 - (int)(__float_as_uint(lift[t]) >> 23);
                 const float keep = exp2f(m[t] - M);
-                if (keep > 0.f) E = max(E, 127 - (int)(__float_as_uint(lift[t]) >> 23) + (int)ceilf(m[t] - M));
-                const float up = __uint_as_float((uint32_t)(127 - E) << 23);
-                const float down = keep * (up / lift[t]);
+                if (keep > 0.f) H = max(H, was + ((int)ceilf(m[t] - M) >> 1));
+                const float up = __uint_as_float((uint32_t)(127 - H) << 23);
+                const float by = __uint_as_float((uint32_t)(127 + was - H) << 23);
+                const float down = keep * by * by;  // (2 at most; by reaches 2^75 where keep is 2^-149)
                 l[t] *= keep;
 #pragma unroll
                 for (int i = 0; i < 2 * VW; ++i)
@@ -345,8 +351,8 @@ struct Heads {
                     for (int e = 0; e < 4; ++e) acc[t][i][e] *= down;
                 m[t] = M;
                 lift[t] = up;
-                w0 = u0 * up * v0;
-                w1 = u1 * up * v1;
+                w0 = u0 * up * v0 * up;
+                w1 = u1 * up * v1 * up;
             }
             l[t] += u0 + u1;
             // column gid of the weights (head gid / 2, part gid % 2) of this lane's value tokens, from
@@ -386,9 +392,9 @@ struct Heads {
             const float L = sum(t);
             if (g >= G) continue;
             typename E::T* o = static_cast<typename E::T*>(a.out) + (row0 + g) * D + gid * (D / 8);
-            const float r = L == 0.f ? 0.f : 1.f / (L * lift[t]);
+            const float r = L == 0.f ? 0.f : 1.f / L, up = inverse_pow2(lift[t]);
 #pragma unroll
-            for (int i = 0; i < 4 * VW; ++i) o[i] = E::from_float(col(t, i) * r);
+            for (int i = 0; i < 4 * VW; ++i) o[i] = E::from_float(col(t, i) * r * up * up);
         }
     }
     // The state as a partial: (max, sum) at ml[g], columns at pa[g D ..].
@@ -399,11 +405,11 @@ struct Heads {
             const float L = sum(t);
             if (g >= G) continue;
             if (gid == 0) ml[g] = make_float2(m[t], L);
-            const float r = 1.f / lift[t];  // to units of 2^m
+            const float up = inverse_pow2(lift[t]);  // twice: to units of 2^m
+            auto full = [&](int i) { return col(t, i) * up * up; };
             float4* o = reinterpret_cast<float4*>(pa + g * D + gid * (D / 8));
 #pragma unroll
-            for (int i = 0; i < VW; ++i)
-                o[i] = make_float4(col(t, 4 * i) * r, col(t, 4 * i + 1) * r, col(t, 4 * i + 2) * r, col(t, 4 * i + 3) * r);
+            for (int i = 0; i < VW; ++i) o[i] = make_float4(full(4 * i), full(4 * i + 1), full(4 * i + 2), full(4 * i + 3));
         }
     }
     __device__ __forceinline__ float sum(int t) const {
