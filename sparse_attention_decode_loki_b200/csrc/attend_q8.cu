@@ -110,9 +110,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// 1 / x of a power of two
-__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
-
 // box {D, 16} of a [rows, D] byte matrix, from its row `row` on
 __device__ __forceinline__ void tile_load(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {
     asm volatile(
@@ -378,6 +375,9 @@ struct Heads {
         }
     }
 
+    // 2^E
+    __device__ __forceinline__ float unit(int t) const { return 1.f / (lift[t] * lift[t]); }
+
     // column i of the lane's, in units of 2^(m + E)
     __device__ __forceinline__ float col(int t, int i) const {
         return acc[t][i >> 1][2 * (i & 1)] + acc[t][i >> 1][2 * (i & 1) + 1];
@@ -392,9 +392,9 @@ struct Heads {
             const float L = sum(t);
             if (g >= G) continue;
             typename E::T* o = static_cast<typename E::T*>(a.out) + (row0 + g) * D + gid * (D / 8);
-            const float r = L == 0.f ? 0.f : 1.f / L, up = inverse_pow2(lift[t]);
+            const float r = L == 0.f ? 0.f : 1.f / L, up = unit(t);
 #pragma unroll
-            for (int i = 0; i < 4 * VW; ++i) o[i] = E::from_float(col(t, i) * r * up * up);
+            for (int i = 0; i < 4 * VW; ++i) o[i] = E::from_float(col(t, i) * r * up);
         }
     }
     // The state as a partial: (max, sum) at ml[g], columns at pa[g D ..].
@@ -405,11 +405,11 @@ struct Heads {
             const float L = sum(t);
             if (g >= G) continue;
             if (gid == 0) ml[g] = make_float2(m[t], L);
-            const float up = inverse_pow2(lift[t]);  // twice: to units of 2^m
-            auto full = [&](int i) { return col(t, i) * up * up; };
+            const float r = unit(t);  // to units of 2^m
             float4* o = reinterpret_cast<float4*>(pa + g * D + gid * (D / 8));
 #pragma unroll
-            for (int i = 0; i < VW; ++i) o[i] = make_float4(full(4 * i), full(4 * i + 1), full(4 * i + 2), full(4 * i + 3));
+            for (int i = 0; i < VW; ++i)
+                o[i] = make_float4(col(t, 4 * i) * r, col(t, 4 * i + 1) * r, col(t, 4 * i + 2) * r, col(t, 4 * i + 3) * r);
         }
     }
     __device__ __forceinline__ float sum(int t) const {
