@@ -81,7 +81,7 @@ constexpr int kClusterTiles = 23680;  // up to so many tiles (ten for every resi
 constexpr int kQ8MaxWarps = 2 * 148 * 16;  // workspace is laid out for at most this many
 constexpr int kTile = 16;
 constexpr uint32_t kNoRow = 0xffffffffu;
-constexpr float kLeast = -3.402823466e38f;  // below every score
+constexpr float kMost = 3.402823466e38f, kLeast = -kMost;  // kLeast: below every score
 
 // D[16x8] += A[16x16] B[16x8], fp16 in, fp32 out
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -318,8 +318,11 @@ struct Heads {
         uint32_t pf[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float x0 = ok0 ? ((c[t][0][0] + c[t][1][0]) + (c[t][0][1] + c[t][1][1])) * qs[t] * k0 : -INFINITY;
-            const float x1 = ok1 ? ((c[t][0][2] + c[t][1][2]) + (c[t][0][3] + c[t][1][3])) * qs[t] * k1 : -INFINITY;
+            // (the scales first: a large query times codes may leave fp32 where the score does not; their own
+            // product only where a code other than zero would)
+            const float f0 = fminf(qs[t] * k0, kMost), f1 = fminf(qs[t] * k1, kMost);
+            const float x0 = ok0 ? ((c[t][0][0] + c[t][1][0]) + (c[t][0][1] + c[t][1][1])) * f0 : -INFINITY;
+            const float x1 = ok1 ? ((c[t][0][2] + c[t][1][2]) + (c[t][0][3] + c[t][1][3])) * f1 : -INFINITY;
             float u0 = exp2_fast(x0 - m[t]), u1 = exp2_fast(x1 - m[t]);
             float w0 = u0 * lift[t] * v0 * lift[t], w1 = u1 * lift[t] * v1 * lift[t];
             const float top = fmaxf(x0, x1);

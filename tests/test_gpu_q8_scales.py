@@ -104,3 +104,14 @@ def test_small_values_among_many_tokens(loki, cuda):
     K8.view(torch.uint8).zero_()
     q = torch.randn(1, 4, 128, generator=torch.Generator().manual_seed(68)).to(cuda)
     compare(loki, torch, q, K8, V8, ks, vs, bt, sl, 32)
+
+
+@pytest.mark.parametrize("qs,s", [(5e37, 1e-38), (1e-37, 5e34)])
+def test_queries_and_keys_of_opposite_sizes(loki, cuda, qs, s):
+    """Scores of ordinary size from queries near one end of fp32 and keys near the other."""
+    import torch
+    n = 300
+    K8, V8, ks, vs, bt, sl = pool(torch, cuda, 2, 128, 32, 16, [n], 11, 69)
+    ks.fill_(s)
+    q = (torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(70)) * qs).to(cuda)
+    compare(loki, torch, q, K8, V8, ks, vs, bt, sl, 16)
