@@ -115,3 +115,48 @@ def test_queries_and_keys_of_opposite_sizes(loki, cuda, qs, s):
     ks.fill_(s)
     q = (torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(70)) * qs).to(cuda)
     compare(loki, torch, q, K8, V8, ks, vs, bt, sl, 16)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40])
+@pytest.mark.parametrize("basis", [False, True], ids=["noP", "P"])
+@pytest.mark.parametrize("old", [0.0, 0.3, 0.0071, 1.9 * 2.0 ** 30, 1.7 * 2.0 ** 126, 3.0 * 2.0 ** -140])
+def test_appends_behind_blocks_of_any_scale(loki, cuda, T, basis, old):
+    """Older tokens of a block whose scale is no power of two: it stays, or its codes move to the new one."""
+    import torch
+    H, D, page, block, pos = 2, 128, 32, 16, 11
+    g = torch.Generator().manual_seed(72)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(cuda)  # noqa: E731
+    n = -(-(pos + T) // page)
+    K, V = rnd(1, H, T, D), rnd(1, H, T, D)
+    P = torch.linalg.qr(torch.randn(H, D, D, generator=g))[0].contiguous().to(cuda) if basis else None
+    K8, V8 = ((rnd(n, H, page, D) * 80).to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.full((n, H, page // block), old, device=cuda) for _ in range(2))
+    bt = torch.arange(n, dtype=torch.int32, device=cuda)[None].contiguous()
+    was = [t.double().cpu().numpy() for t in (K8, V8)]
+    loki.loki_append_keys_paged_q8(K, V, P, K8, V8, ks, vs, bt, torch.tensor([pos], dtype=torch.int32, device=cuda))
+    torch.cuda.synchronize()
+    assert loki.loki_device_error(reset=True) == 0
+    x = K.double().cpu().numpy()[0]
+    p = None if P is None else P.double().cpu().numpy()
+    rows = (x if p is None else np.einsum("htd,hdc->htc", x, p), V.double().cpu().numpy()[0])
+    # fp32 keys: D products of 22-bit parts summed with the basis; the values are exact
+    bound = (0.0 if p is None else (D + 4) * 2.0 ** -24 * np.abs(x).max() * np.abs(p).sum(1).max(), 0.0)
+    old32 = float(np.float32(old))
+    for codes, scales, before, x, b in zip((K8, V8), (ks, vs), was, rows, bound):
+        got, sc = codes.double().cpu().numpy(), scales.double().cpu().numpy()
+        for h in range(H):
+            for a in range(0, pos + T, block):
+                first, z = max(pos - a, 0) % block if a <= pos else 0, min(a + block, pos + T)
+                y = x[h, a + first - pos:z - pos]
+                c0 = before[a // page, h, a % page:a % page + block]
+                want, s = q8_ref.append_block(c0, old32, y, first)
+                assert sc[a // page, h, a % page // block] == s
+                c = got[a // page, h, a % page:a % page + block]
+                # the exact quotient moved by the bound and by the roundings of a reciprocal (or of the scales'
+                # quotient) and of a product, 2^-23 of it: the code lies between the two ends' codes
+                for part, exact, off in ((slice(0, first), c0[:first] * (old32 / s) if s > old32 else c0[:first], 0.0),
+                                         (slice(first, first + len(y)), y / s, b / s)):
+                    off = off + 2.0 ** -23 * np.abs(exact) * (1.0 + 2.0 ** 4 * (s > 2.0 ** 126))  # (subnormal reciprocals)
+                    lo, hi = q8_ref.e4m3_round(exact - off), q8_ref.e4m3_round(exact + off)
+                    assert np.all((c[part] >= lo) & (c[part] <= hi)), (h, a, part)
+                assert np.array_equal(c[first + len(y):], c0[first + len(y):])
