@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kCdThreads, 2) k_decode_cluster(
             bad = true;
             break;
         }
-        // every thread is done with stage st: refill it
+        // every thread is done with stage st (its keys, stored above, hang on every word it read): refill it
         if (tid == 0 && t + kCdStages < ntiles) issue(t + kCdStages);
     }
     if (bad && tid == 0)

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kFusedThreads, MINB) k_decode_fused(
             bad = true;
             break;
         }
-        // every thread is done with stage st: refill it
+        // every thread is done with stage st (its keys, stored above, hang on every word it read): refill it
         if (tid == 0 && t + kFusedStages < ntiles) issue(t + kFusedStages);
     }
     if (bad) {

@@ -259,6 +259,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) k_score_paged(
 #pragma unroll
                 for (int g = 0; g < G; ++g) srow[(int64_t)g * S_cap + t0 + tid] = a[g];
             }
+            // The row's scores, stored above, hang on every word read from the slot: the reads are done
+            // before the arrival, and the next copy follows it. (A reader that still holds loads in flight
+            // there would need fence.proxy.async, which costs 0.5 % of a scan here.)
             __syncwarp();
             if (lane == 0 && !bad) mbar_arrive(&empty[stg]);
         }

@@ -279,6 +279,9 @@ __device__ __forceinline__ void score_plane_body(
 #pragma unroll
                 for (int g = 0; g < G; ++g) srow[(int64_t)g * S + t0 + tid] = a[g];
             }
+            // The row's scores, stored above, hang on every word read from the slot: the reads are done
+            // before the arrival, and the next copy follows it. (A reader that still holds loads in flight
+            // there would need fence.proxy.async, which costs 0.5 % of a scan here.)
             __syncwarp();
             if (lane == 0 && !bad) mbar_arrive(&empty[st]);
         }
@@ -343,7 +346,7 @@ __device__ __forceinline__ void score_plane_body(
 #pragma unroll
             for (int g = 0; g < G; ++g) scores[(qrow0 + g) * S + x] = a[g];
         }
-        __syncwarp();
+        __syncwarp();  // (as above: the scores are stored, so the slot is read)
         if (lane == 0 && !bad) mbar_arrive(&empty[st]);
     }
 }
