@@ -108,6 +108,11 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_s
     __shared__ __align__(8) uint64_t full[kStThreads / 32][kStQueryStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7, sub = lane >> 3;
     const bool lane_on = u < a.D >> 4;
+    // A programmatic dependent of the keys' kernel, which writes nothing that is read or written here.
+    // What is read here came before that kernel, and every CTA of it has waited for that work (griddep_wait)
+    // before it releases its dependents: it is complete, and no line of it is older, when this grid starts.
+    // (A wait of its own would wait for the keys as well. Fences on both sides: 42.0 us instead of 39.3 for
+    // four ragged prompts up to 2048 tokens of 32 query and 8 KV heads; every read from the L2: 41.0.)
     if ((int)blockIdx.x >= a.kv_ctas) {
         // CTAs side by side take rows side by side
         const int q = blockIdx.x - a.kv_ctas, blocks = (a.T + kStQueryRows - 1) / kStQueryRows, b = q / blocks % a.B;
@@ -246,8 +251,8 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_s
             }
         }
     }
-    // A programmatic dependent of the keys' kernel, which it shares no data with: the grid must end
-    // after it, so one CTA waits (the others would hold their places on the SMs).
+    // The grid must end after the keys' kernel, for those who wait for this one: one CTA waits (the
+    // others would hold their places on the SMs).
     if (blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 

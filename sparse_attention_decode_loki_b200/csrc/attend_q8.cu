@@ -799,7 +799,10 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, kCl ? 2 : 4) k_
 
 // Merges the partials of one (sequence, query head) row: the W warps take
 // partials in turn, four columns a lane. Rows that one warp owned whole are
-// written already; rows without tokens get zeros.
+// written already; rows without tokens get zeros. The lengths are read before
+// the wait: they are older than the partials' kernel, every CTA of which has
+// waited for all that came before it when it releases this grid. (With the wait
+// first a call takes 1.3 to 2.3 us longer.)
 template <class E, int D, int W>
 __global__ void __launch_bounds__(32 * W) k_q8_combine(const AttendQ8Args a) {
     __shared__ float sm_m[W], sm_l[W];
@@ -965,7 +968,15 @@ static cudaError_t cluster_slots(const void* kern, size_t smem, ClusterSlots* ou
 //   40 x 16 x 4096 ragged 69 / 79, 8 x 4 x 32768 42 / 49, 32 x 4 x 2048 13 / 19;
 //   8 x 2 x 65536 (43 % of the places filled) 67 / 55, 40 x 8 x 4096 (54 %)
 //   75 / 63, 8 x 1 x 131072 (22 %) 114 / 75; 8 x 1 x 32768 (22 %, but few
-//   tiles) 32 / 38.
+//   tiles) 32 / 38. Around the border, even lengths: 9 x 20 x 8192 (61 %) 77 / 69,
+//   40 x 5 x 8192 (68 %) 78 / 75, 40 x 15 x 4096 (68 %) 118 / 107, 8 x 13 x 16384
+//   (70 %) 80 / 78, 40 x 16 x 4096 (72 %) 119 / 112, 40 x 3 x 16384 (81 %) 82 / 88,
+//   8 x 11 x 16384 (89 %, clusters of three) 61 / 67. Ragged lengths shift it
+//   down: whole units end apart, and others follow them.
+// The tokens are the block table's capacity, the lengths being on the device: a
+// wide table over short sequences takes the two kernels where clusters would do
+// (8 x 24 x 1000 behind a table of 8192 32 us, of 1024 17; one sequence of 513
+// 7.0 to 7.5 us either way).
 // Sizes: meeting the other CTAs costs about a tile's time, so two tiles a warp
 // stay in one CTA (32 units of 16 tiles 5.7 us, in clusters of 2 to 8 6.1) and
 // 64 tiles in four (7.2; in eight 7.6); sizes other than powers of two lose 15 %
