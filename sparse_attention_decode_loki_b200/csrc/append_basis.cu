@@ -149,10 +149,12 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
     unit_cols(turn ? rot : 0, a.interleaved, u, &ca, &cb);
     Chunk<E> wa[4], wb[4];
     uint32_t live = 0;
-    auto load = [&]() {
+    uint32_t angle_loads = 0;  // thread 0's
+    auto load = [&](bool ok) {
         const int64_t start = (sq.lo / kRunRows + run) * kRunRows, j0 = start + 16 * warp + sub;
         const Tp* p = static_cast<const Tp*>(a.K_new) + (((int64_t)b * a.H_kv + hk) * a.T + (j0 - sq.p0)) * D;
-        if (rot > 0 && tid == 0) {  // every reader of the angles before has passed a barrier
+        if (rot > 0 && tid == 0 && ok) {  // every reader of the angles before has passed a barrier
+            ++angle_loads;
             const uint32_t bytes = (uint32_t)min64(sq.hi - start, kRunRows) * rot * 4;
             mbar_arrive_expect_tx(&angle_bar, bytes);
             bulk_load(angles, a.rope + start * rot, bytes, &angle_bar);
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
         sq = append_seq(a, b, false);
         runs = run_count(sq.lo, sq.hi);
         run = (int)(ri - before);
-        load();
+        load(true);
         {
             if (!mbar_wait(&basis_bar, heads & 1, a.err)) alive = false;
             ++heads;
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
                     sq = append_seq(a, b, false);
                     runs = run_count(sq.lo, sq.hi);
                 }
-                load();
+                load(done);
             }
             // this thread's row of the product, half of its columns
             const int r = (warp & 3) * 32 + lane, c0 = (warp >> 2) * DH;
@@ -412,6 +414,12 @@ __global__ void __launch_bounds__(kAbThreads, E::kBytes == 2 ? 2 : 1) k_append_b
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncthreads();  // A and place may be written again
         }
+    }
+    // flagged: copies and products on their way land (or not) before the CTA ends
+    if (!alive && tid == 0) {
+        mbar_wait(&basis_bar, (heads - 1) & 1, a.err);
+        if (angle_loads > 0) mbar_wait(&angle_bar, (angle_loads - 1) & 1, a.err);
+        mbar_wait(&bar, phase ^ 1, a.err);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();

@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 4 : 2) k_append_s
                 o += step;
                 if (++i == S) i = 0, phase ^= 1;
             }
-            // every copy has landed before the CTA may end
-            for (int l = h + 1; l < min(h + S, h1); ++l) {
-                if (++i == S) i = 0, phase ^= 1;
+            // behind a wait that gave up: the copies on their way land (or not) before the CTA may end
+            for (int l = h; l < min(h + S, h1); ++l) {
                 mbar_wait(&full[warp][i], phase, a.err);
+                if (++i == S) i = 0, phase ^= 1;
             }
         }
     } else {
@@ -315,7 +315,10 @@ __global__ void __launch_bounds__(kStThreads, E::kBytes == 2 ? 2 : 1) k_append_k
         if (rot > 0) {
             const bool ok = mbar_wait(&bar, phase, a.err);
             phase ^= 1;
-            if (__syncthreads_or(!ok)) return;
+            if (__syncthreads_or(!ok)) {  // flagged: the copy lands (or not) before the CTA ends
+                mbar_wait(&bar, phase ^ 1, a.err);
+                return;
+            }
         }
         for (int h = h0; h < h1; ++h) {
             const int shift = h * a.page_size;

@@ -633,7 +633,14 @@ __global__ void __launch_bounds__(kCl ? kClThreads : kQ8Threads, NT == 1 ? (kCl 
         if (w + kStages - 1 < w_end) tile[kStages - 1] = load(at == 0 ? kStages - 1 : at - 1);
         const float ks1 = __ldg(a.k_scales + tile[1].blk), vs1 = __ldg(a.v_scales + tile[1].blk);
         alive = mbar_wait(bar + at, phase, a.err);
-        if (!__all_sync(0xffffffffu, alive)) break;  // flagged; nothing waits for the rest
+        if (!__all_sync(0xffffffffu, alive)) {  // flagged: the copies on their way land (or not) before the ring is left
+#pragma unroll 1
+            for (int i = 0; i < kStages && w + i < w_end; ++i) {
+                const int s = at + i;
+                mbar_wait(bar + (s < kStages ? s : s - kStages), phase ^ (s >= kStages), a.err);
+            }
+            break;
+        }
         const int valid = tile[0].valid;
         if (valid > 0)
             h.add(ring[at], tk < valid, tk + 8 < valid, ks, ks, vs, vs, valid < kTile, valid, lane);
