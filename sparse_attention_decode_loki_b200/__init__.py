@@ -13,12 +13,32 @@ top k are kept, and exact softmax attention runs over those k tokens only.
 """
 from __future__ import annotations
 
+import re
 from typing import Optional, Tuple
 
 import torch
 
 from ._lib import DTYPE_BF16, DTYPE_F32, LIB_PATH, LokiError, check, lib  # noqa: F401
-from . import _binding as _b  # built beside libloki.so by build.py
+
+
+class _NoBinding:
+    """Stands for the compiled binding where it cannot be used: the calls that need it say why."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        raise ImportError(f"the compiled binding of the paged 8-bit and rotary calls cannot be used ({self._why}): "
+                          "build it with `python sparse_attention_decode_loki_b200/build.py`")
+
+
+try:
+    from . import _binding as _b  # built beside libloki.so by build.py
+    _made_for = getattr(_b, "torch_version", "of another version")  # (major.minor.patch; it reads torch's own classes)
+    if re.split(r"(?<=\d)(?:[^\d.]|\.dev)", torch.__version__)[0] != _made_for:
+        _b = _NoBinding(f"built for torch {_made_for}, this is {torch.__version__}")
+except ImportError as e:  # absent, or of another torch or interpreter; every other call needs libloki.so alone
+    _b = _NoBinding(str(e))
 
 __all__ = [
     "LokiError", "LIB_PATH",
@@ -72,8 +92,9 @@ def _expect(t: torch.Tensor, shape, dtype, name: str) -> None:
         raise ValueError(f"{name} must be {dtype} {list(shape)} (got {t.dtype} {list(t.shape)})")
 
 
-# The raw handle by itself: 0.1 us, where the Stream object around it takes 2.2 us.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The raw handle by itself: 0.1 us, where the Stream object around it takes 2.2 us. (A torch built without
+# CUDA has none; its tensors are refused before a stream is asked for.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(dev: torch.device) -> int:
