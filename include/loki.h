@@ -332,7 +332,7 @@ LOKI_API loki_status loki_rope_table(float* table, int64_t n_pos, int rot_dim, d
  * are turned by their positions' angles and then rotated into the basis,
  * K~ = rope(K_new) P (all fp32, one rounding to dt); values are copied.
  *   K_new, V_new [B, H_kv, T, D] (dt)
- *   P            [H_kv, D, D] fp32, or NULL: no basis, K~ = rope(K_new)
+ *   P            [H_kv, D, D] fp32, finite, or NULL: no basis, K~ = rope(K_new)
  *   rope_table   [n_pos, rot_dim] fp32 as loki_rope_table writes it (or any
  *                other angles), or NULL: no rotary embedding. Columns i and
  *                i + rot_dim / 2 form a pair (interleaved == 0), or columns
@@ -346,8 +346,9 @@ LOKI_API loki_status loki_rope_table(float* table, int64_t n_pos, int rot_dim, d
  *                (clamped to [0, T]) tokens of sequence b are appended; the
  *                others' rows, q_out's among them, are left as they were.
  * Tokens outside the block table, in a page outside the pool (device error 2)
- * or at positions >= n_pos (device error 3) are not written. No two appended
- * tokens may share a cache row. No workspace.
+ * or at positions >= n_pos (device error 3) are not written to the pages; their
+ * queries are turned all the same, but those at positions < 0 or >= n_pos are
+ * left as they were. No two appended tokens may share a cache row. No workspace.
  */
 LOKI_API loki_status loki_append_keys_paged_rope(
     const void* K_new, const void* V_new, const float* P, const float* rope_table, int64_t n_pos,
@@ -387,7 +388,8 @@ LOKI_API size_t dense_decode_paged_q8_workspace_size(int B, int H_q, int H_kv, i
  *   q, out [B, H_q, D] (dt); scale <= 0 selects 1/sqrt(D)
  * q and the cached keys are both in the PCA basis or both not. Tokens in pages
  * outside the pool are skipped (device error 2); a sequence without tokens
- * gives zeros. Scores, softmax and sums in fp32.
+ * gives zeros. Scores, softmax and sums in fp32: a score and 2^8 times the sum
+ * of a sequence's |values| in a column have to stay within it.
  */
 LOKI_API loki_status dense_decode_attention_paged_q8(
     const void* q, const void* K8_pages, const void* V8_pages, const float* k_scales,

@@ -4,9 +4,9 @@
 //
 // The product is 2 D flop for each of a key's D outputs, and has to come out
 // as fp32 would give it (the plane's scores choose tokens by it). Both sides
-// are carried as two fp16 parts, x = hi + lo (22 bits, after a power of two
-// per row of keys and per column of P has brought the largest entry to
-// 2^14..2^15), and three of the four products are taken: lo hi, hi lo, hi hi;
+// are carried as two fp16 parts, x = hi + lo (after a power of two per row of
+// keys and per column of P has brought the largest entry to 2^14..2^15: 22 bits,
+// or 2^-39 of the largest entry where that is more), and three of the four products are taken: lo hi, hi lo, hi hi;
 // the fourth lies below 2^-22 of the product. So 6 D flop per output, at the
 // fp16 rate with fp32 accumulators in tensor memory.
 //
@@ -16,9 +16,10 @@
 //   D [128 x D] fp32 in tensor memory, read back one row to a lane.
 //
 // A persistent CTA of eight warps takes consecutive tiles with the head slowest,
-// so most keep their P. It leaves half of the SM's registers to the stream of
-// values and queries, which runs beside it as a programmatic dependent: both
-// wait on latencies most of the time. Stores go through shared memory (a lane
+// so most keep their P. In bf16 it leaves half of the SM's registers to the stream
+// of values and queries, which runs beside it as a programmatic dependent: both
+// wait on latencies most of the time. (fp32 rows in flight take 216 to 255 registers
+// a thread, the whole SM: there the stream fills it as the tiles' CTAs end.) Stores go through shared memory (a lane
 // holds one row: stored directly, each 16 bytes would touch another line, which
 // took 1.5 us a tile). Rows that hold an infinity or a NaN take the plain fp32
 // sum instead (an infinity has no second part).

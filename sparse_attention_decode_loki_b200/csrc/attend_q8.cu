@@ -17,8 +17,9 @@
 //
 // An fp32 query or weight is carried as two fp16 parts, value = hi + lo, in
 // neighbouring columns (an accumulator's two columns belong to one lane, which
-// adds them): 22 bits, after a power of two has brought the row's largest entry
-// to 2^14..2^15, so entries down to 2^-29 of it keep all 22. One such
+// adds them), after a power of two has brought the row's largest entry to
+// 2^14..2^15: 22 bits down to 2^-17 of it; smaller entries are off by 2^-25,
+// fp16's last place, at most, which is 2^-39 of the largest. One such
 // instruction has room for four heads; five to eight take two. (8-bit operands
 // would halve the instructions, but carry four bits of a query at a time.)
 //
@@ -52,7 +53,7 @@
 // merges. Either way which warp reduces which tiles is fixed by sizes alone.
 //
 // Measured, inputs in DRAM: 16 ragged sequences to 4096 tokens, 40 heads, 436 MB
-// in 69 to 76 us (6.0 TB/s; 69 without any arithmetic in the two-kernel form);
+// in 71 to 77 us (6.0 TB/s; 69 without any arithmetic in the two-kernel form);
 // 4 x 32768 tokens, 8 KV heads for 32, 218 MB in 43 us; 512 selected tokens for
 // each of 640 rows, 79 MB of random 128-byte rows in 25 us (21 without
 // arithmetic); one sequence of 513 tokens, 32 heads, 6.8 us.
